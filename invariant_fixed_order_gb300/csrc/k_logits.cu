@@ -79,6 +79,10 @@ log_softmax_partial_kernel(const float* __restrict__ x, int32_t V, int32_t nseg,
             const int32_t j = seg * kSeg + tid + kSegThreads * k;
             if (j < V) z = __fadd_rn(z, expf(__fsub_rn(v[k], m)));
         }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k)
+            if (isnan(v[k])) z = v[k];
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) z = __fadd_rn(z, __shfl_xor_sync(0xffffffffu, z, off));
@@ -494,6 +498,10 @@ __device__ __forceinline__ void logprobs_segment(const IN* __restrict__ xr, int3
                 t = __fmaf_rn(expf(d), fmaxf(d, -FLT_MAX), t);
             }
         }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k)
+            if (isnan(v[k])) z = v[k];
     }
     // (a NaN column makes this thread's sum NaN, where there is one)
     const bool odd = m == -INFINITY || isnan(z);
@@ -582,7 +590,7 @@ __device__ __forceinline__ RowSums row_sums(const float4* __restrict__ pr, int32
             const float d = __fsub_rn(p.x, m), f = expf(d);
             pz = __fmul_rn(p.y, f);
             // a segment without a finite logit, or too far below m to weigh anything, adds nothing (d may be
-            // as low as -FLT_MAX: z_s d overflows)
+            // as low as -FLT_MAX: z_s d overflows); a NaN reaches the entropy through z
             pt = p.y == 0.0f || f == 0.0f ? 0.0f : __fmul_rn(f, __fmaf_rn(p.y, d, p.z));
         }
         const int n = min(32, nseg - s0);
