@@ -401,9 +401,8 @@ bi_status bi_qk_norm_rope_append(const void* qkv, bi_dtype qkv_dtype, const bi_b
  * Positions a node does not attend contribute nothing, whatever the cache
  * holds there (NaN and infinities included).
  * Arithmetic: scores in fp32 (bf16 products), softmax statistics and sums in
- * fp32; the weights p = 2^(score - reference) multiply V as bf16 hi + lo parts
- * where out is fp32, rounded once to bf16 where it is bf16.  A request's
- * positions are cut into at most BI_TREE_MAX_SEGMENTS segments of whole 128
+ * fp32; the weights p = 2^(score - reference) multiply V as bf16 hi + lo parts;
+ * a bf16 output is the fp32 output, rounded once.  A request's positions are cut into at most BI_TREE_MAX_SEGMENTS segments of whole 128
  * positions, walked 64 at a time, whose results are folded in ascending order;
  * the cut follows from its positions, nodes, H and Hkv, so a row's bits are its
  * request's.

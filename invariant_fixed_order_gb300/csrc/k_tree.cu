@@ -16,11 +16,11 @@
 //                          M) is then applied to O and L)
 //   L = L + sum p          fp32, of the unrounded p
 //   O = O + P V            tcgen05 128 x Dh x 16 keys, accumulated in TMEM
-// fp32 outputs take P as bf16 hi + lo parts (p to 2^-16); bf16 outputs take one
-// bf16 part: its rounding, at most 2^-8 of each p, is of the size of the
-// output's own (2^-8), and the second part cost 8 / 20 / 18 % (16 requests /
-// 64 / long contexts, below).  A segment's M, L and O go to the workspace and
-// tree_merge_kernel folds them in ascending order,
+// P is taken as bf16 hi + lo parts (p to 2^-16), as in the decode and prefill
+// kernels: one part would be off by up to 2^-8 of each p, which over few keys is
+// as much as a bf16 output's own rounding.  Outputs of either type are the same
+// fp32 values, rounded once where they are bf16.  A segment's M, L and O go to
+// the workspace and tree_merge_kernel folds them in ascending order,
 //   M' = max(M, m), L' = L 2^(M-M') + l 2^(m-M'), O' likewise.
 // All of that belongs to the request alone.  Which CTA computes a segment does
 // not: the launch's segments, laid end to end, are cut into one contiguous range
@@ -533,7 +533,7 @@ __device__ __forceinline__ void commit_elected(uint64_t* bar) {
 // the scores take the buffer whose P was multiplied just before them, in order.
 // Every stage of K and V is waited for and let go by both lanes, in turn, so
 // that none can take one fill's phase for another's.
-template <int DH, bool kLo>
+template <int DH>
 __device__ __forceinline__ void issue_products(Smem<DH>& sm, uint32_t tmem, int lane_id) {
     constexpr int kStagesK = Smem<DH>::kStagesK, kStagesV = Smem<DH>::kStagesV;
     constexpr uint32_t kUnit = 16;  // a descriptor's address field counts 16 bytes: steps of an operand are added to it
@@ -618,8 +618,8 @@ __device__ __forceinline__ void issue_products(Smem<DH>& sm, uint32_t tmem, int 
                 const uint32_t p = col_s + buf * kHalf;
                 auto product = [&](int ks) {  // of 16 keys: the hi part, then the lo part
                     const uint64_t v = vd + ks * (DH / 64 * BI_PAGE * 128) / kUnit;
-                    mma_ts_elected(col_o, p + (kLo ? 16 : 8) * ks, v, idesc_pv, ks > 0 || h > 0);
-                    if constexpr (kLo) mma_ts_elected(col_o, p + 16 * ks + 8, v, idesc_pv, 1u);
+                    mma_ts_elected(col_o, p + 16 * ks, v, idesc_pv, ks > 0 || h > 0);
+                    mma_ts_elected(col_o, p + 16 * ks + 8, v, idesc_pv, 1u);
                 };
                 const int ksteps = (min(kHalf, keys - h * kHalf) + 15) / 16;
                 if (ksteps == kHalf / 16) {
@@ -669,10 +669,9 @@ __device__ __forceinline__ void tmem_st_f32(uint32_t taddr, const float (&v)[32]
 // joins warps but mbarriers with bounded waits: a warp whose wait runs out sets
 // abort and leaves, and the others follow.
 // ---------------------------------------------------------------------------
-template <int G, int DH, bool kLo>
+template <int G, int DH>
 __device__ __forceinline__ void consume(Smem<DH>& sm, uint32_t tmem, const TreeArgs& a, const Layout& lay) {
     constexpr int kStagesV = Smem<DH>::kStagesV;
-    constexpr int kGroup = kLo ? 16 : 8;  // columns that the P of 16 keys takes
     const int tid = threadIdx.x, lane = tid & 31, lane_id = tid / 128, lq = (tid / 32) & 3;
     const int row = tid & 127;  // = its tensor-memory lane
     const float c = __fmul_rn(a.scale, 1.44269504088896341f);
@@ -758,21 +757,16 @@ __device__ __forceinline__ void consume(Smem<DH>& sm, uint32_t tmem, const TreeA
                             e.x = ex2(e.x);
                             e.y = ex2(e.y);
                             acc[x & 1] = add2(acc[x & 1], e);
-                            if constexpr (kLo) {
-                                pack_p(e.x, e.y, hi[x], lo[x]);
-                            } else {
-                                const __nv_bfloat162 r = __floats2bfloat162_rn(e.x, e.y);
-                                hi[x] = *reinterpret_cast<const uint32_t*>(&r);
-                            }
+                            pack_p(e.x, e.y, hi[x], lo[x]);
                         }
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
-                            s[g / 16 * kGroup + x] = hi[x];
-                            if constexpr (kLo) s[g + 8 + x] = lo[x];
+                            s[g + x] = hi[x];
+                            s[g + 8 + x] = lo[x];
                         }
                     }
                     tmem_st32(col_s, s);
-                    if constexpr (kLo) tmem_st32(col_s + 32, s + 32);
+                    tmem_st32(col_s + 32, s + 32);
                     const float2 t = add2(acc[0], acc[1]);
                     L = __fadd_rn(L, __fadd_rn(t.x, t.y));
                 }
@@ -891,7 +885,7 @@ __device__ __forceinline__ void consume(Smem<DH>& sm, uint32_t tmem, const TreeA
     }
 }
 
-template <int G, int DH, bool kLo>
+template <int G, int DH>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, TreeArgs a, Layout lay) {
@@ -945,9 +939,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     if (warp >= kSoftWarps) {
         if (warp == kSoftWarps) produce<G, DH, true>(sm, &tmK, &tmV, &tmQ, a, lay.slots);
         else if (warp == kSoftWarps + 2) produce<G, DH, false>(sm, &tmK, &tmV, nullptr, a, lay.slots);
-        else issue_products<DH, kLo>(sm, tmem, warp == kSoftWarps + 1 ? 0 : 1);
+        else issue_products<DH>(sm, tmem, warp == kSoftWarps + 1 ? 0 : 1);
     } else {
-        consume<G, DH, kLo>(sm, tmem, a, lay);
+        consume<G, DH>(sm, tmem, a, lay);
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -1069,7 +1063,7 @@ static int32_t launch_rows(int32_t max_nodes, int32_t G) {
 static size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 static int32_t launch_slots(int32_t max_seq, int32_t Hkv) { return most_segments((max_seq - 1) / kStep + 1, Hkv); }
 
-template <int G, int DH, bool kLo>
+template <int G, int DH>
 cudaError_t launch_kernel(const TreeArgs& a, const Layout& lay, unsigned ctas, const CUtensorMap& tmK,
                           const CUtensorMap& tmV, const CUtensorMap& tmQ, cudaStream_t s) {
     const size_t smem = sizeof(Smem<DH>);
@@ -1077,11 +1071,11 @@ cudaError_t launch_kernel(const TreeArgs& a, const Layout& lay, unsigned ctas, c
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [smem] {
-        attr_err = cudaFuncSetAttribute(tree_attention_kernel<G, DH, kLo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr_err = cudaFuncSetAttribute(tree_attention_kernel<G, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(smem));
     });
     if (attr_err != cudaSuccess) return attr_err;
-    return launch_pdl(tree_attention_kernel<G, DH, kLo>, dim3(ctas), dim3(kThreads), smem, s, tmK, tmV, tmQ, a, lay);
+    return launch_pdl(tree_attention_kernel<G, DH>, dim3(ctas), dim3(kThreads), smem, s, tmK, tmV, tmQ, a, lay);
 }
 
 template <int G, int DH>
@@ -1097,8 +1091,7 @@ cudaError_t launch(const TreeArgs& a, void* ws, cudaStream_t s) {
     char* w = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(ws)));
     lay.ml = reinterpret_cast<float2*>(w);
     lay.o = reinterpret_cast<float4*>(w + align_up(static_cast<size_t>(tiles) * slots * lay.rows * sizeof(float2)));
-    const cudaError_t e = a.out_f32 ? launch_kernel<G, DH, true>(a, lay, ctas, tmK, tmV, tmQ, s)
-                                    : launch_kernel<G, DH, false>(a, lay, ctas, tmK, tmV, tmQ, s);
+    const cudaError_t e = launch_kernel<G, DH>(a, lay, ctas, tmK, tmV, tmQ, s);
     if (e != cudaSuccess) return e;
     // one block for all dims of its rows, or, while that leaves SMs without one, a block for each 32
     const bool few = tiles * (lay.rows / kMergeRows) < 4 * num_sms();

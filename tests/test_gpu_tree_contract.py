@@ -1,9 +1,10 @@
 """What the header promises of the operators that serve a tree of drafted tokens, at the calls where it is easiest to
 break: logits that are not finite alone in their segment, the two output types, token rows behind the last token."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_tree import INF, NAN, normal
+from test_gpu_tree import HEADS, INF, NAN, TREE_F32, TreeCase, close, normal, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +55,33 @@ def test_log_softmax_of_a_nan_logit(bi, V):
     want = torch.log_softmax(x[4].double(), -1)
     f = torch.isfinite(want)
     assert torch.equal(torch.isfinite(lp[4]), f) and (lp[4][f].double() - want[f]).abs().max() < 1e-5
+
+
+# ---- the output types of the attention --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,Hkv,Dh", HEADS)
+@pytest.mark.parametrize("ctx,nodes", [([0, 3, 1], [1, 2, 5]), ([700, 0, 16, 1999], [7, 64, 33, 31]), ([5000, 40], [100, 256])])
+def test_a_bf16_output_is_the_fp32_output_rounded(bi, H, Hkv, Dh, ctx, nodes):
+    c = TreeCase(ctx, nodes, H, Hkv, Dh, 40 + H)
+    f = c.run(bi, out_dtype=bi.F32)
+    b = c.run(bi)
+    close(f, c.ref(), torch.float32)
+    assert b.dtype == torch.bfloat16 and same_bits(b, f.to(torch.bfloat16))
+    # so it is off by its own rounding and what the fp32 output may be off by
+    ref = c.ref()
+    assert ((b.cpu().double() - ref).abs() <= TREE_F32 * (1 + 2.0 ** -8) + ref.abs() * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("H,Hkv,Dh", [(32, 8, 128), (8, 1, 64), (3, 3, 64)])
+def test_bf16_outputs_repeat_over_many_short_requests(bi, H, Hkv, Dh):
+    rng = np.random.default_rng(4)
+    ctx, nodes = rng.integers(0, 500, 200), rng.integers(0, 5, 200) * rng.integers(0, 20, 200)
+    c = TreeCase(ctx.tolist(), nodes.tolist(), H, Hkv, Dh, 41)
+    st = bi.new_status()
+    first = c.run(bi, status=st).clone()
+    assert same_bits(first, c.run(bi, out_dtype=bi.F32, status=st).to(torch.bfloat16))
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        differ += (c.run(bi, status=st) != first).sum()
+    assert int(differ) == 0
+    bi.check_status(st)
