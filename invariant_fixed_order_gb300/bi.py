@@ -4,6 +4,10 @@ Argument marshalling only: every step of the forward path runs in the CUDA
 library.  PyTorch provides device memory and streams.  Importing this module
 loads ``_build/libbi.so`` and raises if it has not been built — there is no
 fallback path.
+
+``stream=``: the torch.cuda.Stream a call runs on (None: the current one).  The
+call's inputs have to be ready for that stream and its outputs waited for, as
+for any work on another stream; what the call allocates is ordered for it.
 """
 from __future__ import annotations
 
@@ -129,6 +133,23 @@ def _stream(stream=None):
     return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
+def _empty(stream, *shape, dtype, device):
+    """Memory of a call that runs on `stream` (None: the current one), from that stream's pool: a freed block goes to
+    later work of the stream it was taken on, behind the work that used it."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def _result(stream, *shape, dtype, device):
+    """As _empty, for an output: the caller may read it on the current stream (after a wait) and let it go there."""
+    t = _empty(stream, *shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def version() -> int:
     return int(_lib.bi_version())
 
@@ -197,7 +218,7 @@ def _out_dt(c_dtype: int):
 def rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, out: torch.Tensor | None = None,
             stream=None) -> torch.Tensor:
     d = x.shape[-1]
-    out = torch.empty_like(x) if out is None else out
+    out = _result(stream, *x.shape, dtype=x.dtype, device=x.device) if out is None else out
     _shape(gamma, "gamma", d)
     _shape(out, "out", *x.shape)
     _check(_lib.bi_rmsnorm(_d(x, "x", _BF16), _d(gamma, "gamma", _BF16), _d(out, "out", _BF16), x.numel() // d, d,
@@ -218,12 +239,12 @@ def gemm(A: torch.Tensor, W: torch.Tensor, out: torch.Tensor | None = None, c_dt
     N = W.shape[0]
     ncol = N // 2 if ep == EP_SWIGLU else N
     if out is None:
-        out = torch.empty(M, ncol, device=A.device, dtype=torch.float32 if c_dtype == F32 else torch.bfloat16)
+        out = _result(stream, M, ncol, device=A.device, dtype=torch.float32 if c_dtype == F32 else torch.bfloat16)
     _shape(out, "out", M, ncol)
     _shape(residual, "residual", M, N, optional=True)
     need = gemm_workspace_size(M, N, K, mode)
     if need and (ws is None or ws.numel() < need):
-        ws = torch.empty(need, dtype=torch.uint8, device=A.device)
+        ws = _empty(stream, need, dtype=torch.uint8, device=A.device)
     _check(_lib.bi_gemm(_d(A, "A", _BF16), _d(W, "W", _BF16), _d(out, "out", _out_dt(c_dtype)), c_dtype,
                         _d(residual, "residual", _BF16, optional=True), ep, M, N, K, mode,
                         _d(ws, "ws", optional=True), 0 if ws is None else ws.numel() * ws.element_size(),
@@ -248,7 +269,7 @@ def pack_gate_up(w_gate: torch.Tensor, w_up: torch.Tensor, stream=None) -> torch
     _shape(w_gate, "w_gate", None, None)
     F, d = w_gate.shape
     _shape(w_up, "w_up", F, d)
-    out = torch.empty(2 * F, d, dtype=torch.bfloat16, device=w_gate.device)
+    out = _result(stream, 2 * F, d, dtype=torch.bfloat16, device=w_gate.device)
     _check(_lib.bi_pack_gate_up(_d(w_gate, "w_gate", _BF16), _d(w_up, "w_up", _BF16), _d(out, "out", _BF16), F, d,
                                 _stream(stream)))
     return out
@@ -306,11 +327,11 @@ def decode_attention(q, k_cache, v_cache, page_table, seq_lens, max_seq_len: int
     _shape(page_table, "page_table", B, None)
     _shape(seq_lens, "seq_lens", B)
     if out is None:
-        out = torch.empty(B, H, Dh, device=q.device, dtype=torch.float32 if out_dtype == F32 else torch.bfloat16)
+        out = _result(stream, B, H, Dh, device=q.device, dtype=torch.float32 if out_dtype == F32 else torch.bfloat16)
     _shape(out, "out", B, H, Dh)
     need = decode_attention_workspace_size(B, H, Dh, max_seq_len, mode)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _empty(stream, need, dtype=torch.uint8, device=q.device)
     _check(_lib.bi_decode_attention(_d(q, "q", _BF16), _d(k_cache, "k_cache", _BF16), _d(v_cache, "v_cache", _BF16),
                                     _d(page_table, "page_table", _I32), _d(seq_lens, "seq_lens", _I32),
                                     _d(out, "out", _out_dt(out_dtype)), out_dtype, B, H, Hkv, Dh,
@@ -336,7 +357,7 @@ def decode_attention_noalloc(q, k_cache, v_cache, page_table, seq_lens, max_seq_
     _shape(page_table, "page_table", B, None)
     _shape(seq_lens, "seq_lens", B)
     if out is None:
-        out = torch.empty(B, H, Dh, device=q.device, dtype=torch.float32 if out_dtype == F32 else torch.bfloat16)
+        out = _result(stream, B, H, Dh, device=q.device, dtype=torch.float32 if out_dtype == F32 else torch.bfloat16)
     _shape(out, "out", B, H, Dh)
     _check(_lib.bi_decode_attention_noalloc(_d(q, "q", _BF16), _d(k_cache, "k_cache", _BF16),
                                             _d(v_cache, "v_cache", _BF16), _d(page_table, "page_table", _I32),
@@ -367,11 +388,11 @@ def prefill_attention(q, cu_q, q_pos0, k_cache, v_cache, page_table, out_dtype: 
     if max_seq_len is None:
         max_seq_len = page_table.shape[-1] * PAGE
     if out is None:
-        out = torch.empty(T, H, Dh, device=q.device, dtype=torch.float32 if out_dtype == F32 else torch.bfloat16)
+        out = _result(stream, T, H, Dh, device=q.device, dtype=torch.float32 if out_dtype == F32 else torch.bfloat16)
     _shape(out, "out", T, H, Dh)
     need = prefill_attention_workspace_size(T, H, Dh, max_seq_len, mode)
     if need and (ws is None or ws.numel() < need):
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _empty(stream, need, dtype=torch.uint8, device=q.device)
     _check(_lib.bi_prefill_attention(_d(q, "q", _BF16), _d(cu_q, "cu_q", _I32), _d(q_pos0, "q_pos0", _I32),
                                      _d(k_cache, "k_cache", _BF16), _d(v_cache, "v_cache", _BF16),
                                      _d(page_table, "page_table", _I32), _d(out, "out", _out_dt(out_dtype)), out_dtype,
@@ -385,7 +406,7 @@ def prefill_attention(q, cu_q, q_pos0, k_cache, v_cache, page_table, out_dtype: 
 def argmax(logits: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     _shape(logits, "logits", None, None)
     R, V = logits.shape
-    out = torch.empty(R, dtype=torch.int32, device=logits.device) if out is None else out
+    out = _result(stream, R, dtype=torch.int32, device=logits.device) if out is None else out
     _shape(out, "out", R)
     _check(_lib.bi_argmax(_d(logits, "logits", _F32), _d(out, "out", _I32), R, V, _stream(stream)))
     return out
@@ -399,11 +420,11 @@ def log_softmax(logits: torch.Tensor, out: torch.Tensor | None = None, ws: torch
                 stream=None) -> torch.Tensor:
     _shape(logits, "logits", None, None)
     R, V = logits.shape
-    out = torch.empty(R, V, dtype=torch.float32, device=logits.device) if out is None else out
+    out = _result(stream, R, V, dtype=torch.float32, device=logits.device) if out is None else out
     _shape(out, "out", R, V)
     need = log_softmax_workspace_size(R, V)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=logits.device)
+        ws = _empty(stream, max(need, 1), dtype=torch.uint8, device=logits.device)
     _check(_lib.bi_log_softmax(_d(logits, "logits", _F32), _d(out, "out", _F32), R, V, _d(ws, "ws"),
                                ws.numel() * ws.element_size(), _stream(stream)))
     return out
@@ -419,12 +440,12 @@ def sample(logits: torch.Tensor, seeds: torch.Tensor, positions: torch.Tensor, t
     temperatures fp32, all DEVICE [R]."""
     _shape(logits, "logits", None, None)
     R, V = logits.shape
-    out = torch.empty(R, dtype=torch.int32, device=logits.device) if out is None else out
+    out = _result(stream, R, dtype=torch.int32, device=logits.device) if out is None else out
     for name, t in (("seeds", seeds), ("positions", positions), ("temperatures", temperatures), ("out", out)):
         _shape(t, name, R)
     need = sample_workspace_size(R, V)
     if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=logits.device)
+        ws = _empty(stream, max(need, 1), dtype=torch.uint8, device=logits.device)
     _check(_lib.bi_sample(_d(logits, "logits", _F32), _d(seeds, "seeds", _U32), _d(positions, "positions", _I32),
                           _d(temperatures, "temperatures", _F32), _d(out, "out", _I32), R, V, _d(ws, "ws"),
                           ws.numel() * ws.element_size(), _stream(stream)))
@@ -436,7 +457,7 @@ def embed(E: torch.Tensor, ids: torch.Tensor, status=None, out=None, stream=None
     V, d = E.shape
     _shape(ids, "ids", None)
     T = ids.shape[0]
-    out = torch.empty(T, d, dtype=torch.bfloat16, device=E.device) if out is None else out
+    out = _result(stream, T, d, dtype=torch.bfloat16, device=E.device) if out is None else out
     _shape(out, "out", T, d)
     _check(_lib.bi_embed(_d(E, "E", _BF16), _d(ids, "ids", _I32), _d(out, "out", _BF16), T, V, d,
                          _d(status, "status", _I32, optional=True), _stream(stream)))
@@ -491,10 +512,10 @@ def build_slots(q_len, pos0, page_table, free_pages, free_head, T: int, num_page
     _shape(q_len, "q_len", None)
     B, dev = q_len.shape[0], q_len.device
     free_head_out = free_head if free_head_out is None else free_head_out
-    cu_q = torch.empty(B + 1, dtype=torch.int32, device=dev) if cu_q is None else cu_q
-    tok_req = torch.empty(T, dtype=torch.int32, device=dev) if tok_req is None else tok_req
-    tok_pos = torch.empty(T, dtype=torch.int32, device=dev) if tok_pos is None else tok_pos
-    slots = torch.empty(T, dtype=torch.int32, device=dev) if slots is None else slots
+    cu_q = _result(stream, B + 1, dtype=torch.int32, device=dev) if cu_q is None else cu_q
+    tok_req = _result(stream, T, dtype=torch.int32, device=dev) if tok_req is None else tok_req
+    tok_pos = _result(stream, T, dtype=torch.int32, device=dev) if tok_pos is None else tok_pos
+    slots = _result(stream, T, dtype=torch.int32, device=dev) if slots is None else slots
     q, p0, table, free, head, out, dep, cu, req, pos, slot, st = _args(
         ("q_len", q_len, _I32, (B,), False), ("pos0", pos0, _I32, (B,), False),
         ("page_table", page_table, _I32, (B, None), False), ("free_pages", free_pages, _I32, (None,), False),
@@ -547,10 +568,10 @@ def tree_attention(q, cu_q, pos0, tree_mask, k_cache, v_cache, page_table, max_n
     if max_seq_len is None:
         max_seq_len = page_table.shape[1] * PAGE
     if out is None:
-        out = torch.empty(T, H, Dh, device=q.device, dtype=torch.float32 if out_dtype == F32 else torch.bfloat16)
+        out = _result(stream, T, H, Dh, device=q.device, dtype=torch.float32 if out_dtype == F32 else torch.bfloat16)
     need = _lib.bi_tree_attention_workspace_size(B, T, H, cache[1], Dh, max_nodes, max_seq_len)
     if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _empty(stream, need, dtype=torch.uint8, device=q.device)
     pq, cu, p0, mask, k, v, table, po, pw, st = _args(
         ("q", q, _BF16, None, False), ("cu_q", cu_q, _I32, None, False), ("pos0", pos0, _I32, (B,), False),
         ("tree_mask", tree_mask, _U32, None, False), ("k_cache", k_cache, _BF16, None, False),
@@ -582,12 +603,13 @@ def token_logprobs(logits, tokens=None, top_k: int = 0, want_entropy: bool = Tru
     if (V > 1 and logits.stride(1) != 1) or (R > 1 and logits.stride(0) < V):
         raise ValueError("logits: expected rows of consecutive columns that do not overlap")
     dev = logits.device
-    lp = None if tokens is None else torch.empty(R, P, dtype=torch.float32, device=dev)
-    ent = torch.empty(R, dtype=torch.float32, device=dev) if want_entropy else None
-    ids = torch.empty(R, top_k, dtype=torch.int32, device=dev) if top_k > 0 else None
-    top = torch.empty(R, top_k, dtype=torch.float32, device=dev) if top_k > 0 else None
+    lp = None if tokens is None else _result(stream, R, P, dtype=torch.float32, device=dev)
+    ent = _result(stream, R, dtype=torch.float32, device=dev) if want_entropy else None
+    ids = _result(stream, R, top_k, dtype=torch.int32, device=dev) if top_k > 0 else None
+    top = _result(stream, R, top_k, dtype=torch.float32, device=dev) if top_k > 0 else None
     if ws is None:
-        ws = torch.empty(max(_lib.bi_token_logprobs_workspace_size(R, V, top_k), 1), dtype=torch.uint8, device=dev)
+        need = _lib.bi_token_logprobs_workspace_size(R, V, top_k)
+        ws = _empty(stream, max(need, 1), dtype=torch.uint8, device=dev)
     pw, tok, st = _args(("ws", ws, None, None, False), ("tokens", tokens if P else None, _I32, None, True),
                         ("status", status, _I32, None, True))
     _one_device(logits, ws=ws)

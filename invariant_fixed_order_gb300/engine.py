@@ -7,6 +7,8 @@ runs in libbi; this class only owns memory and marshals arguments.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -74,17 +76,18 @@ class Engine:
              want_logits: bool = True, want_hidden: bool = False, stream=None, logits_out=None, tokens_out=None):
         """One forward step.  token_ids / page_table: device int32 tensors (or
         host arrays, copied here); q_len, pos0, logit_rows: host sequences."""
-        if not isinstance(token_ids, torch.Tensor) or token_ids.device.type != "cuda":
-            token_ids = torch.as_tensor(np.asarray(token_ids, np.int32)).to(self.device)
-        if not isinstance(page_table, torch.Tensor) or page_table.device.type != "cuda":
-            page_table = torch.as_tensor(np.ascontiguousarray(page_table, np.int32)).to(self.device)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # (the copies are the step's own)
+            if not isinstance(token_ids, torch.Tensor) or token_ids.device.type != "cuda":
+                token_ids = torch.as_tensor(np.asarray(token_ids, np.int32)).to(self.device)
+            if not isinstance(page_table, torch.Tensor) or page_table.device.type != "cuda":
+                page_table = torch.as_tensor(np.ascontiguousarray(page_table, np.int32)).to(self.device)
         R = len(logit_rows)
         T = int(sum(int(q) for q in q_len))
         if logits_out is None and want_logits:
-            logits_out = torch.empty(R, self.cfg.V, dtype=torch.float32, device=self.device)
+            logits_out = bi._result(stream, R, self.cfg.V, dtype=torch.float32, device=self.device)
         if tokens_out is None:
-            tokens_out = torch.empty(max(R, 1), dtype=torch.int32, device=self.device)
-        hidden = torch.empty(T, self.cfg.d, dtype=torch.bfloat16, device=self.device) if want_hidden else None
+            tokens_out = bi._result(stream, max(R, 1), dtype=torch.int32, device=self.device)
+        hidden = bi._result(stream, T, self.cfg.d, dtype=torch.bfloat16, device=self.device) if want_hidden else None
         self.model.forward_step(q_len, pos0, token_ids, page_table, self.k, self.v, logit_rows, self.ws,
                                 self.status, logits_out=logits_out, tokens_out=tokens_out, hidden_out=hidden,
                                 mode=mode, stream=stream)

@@ -85,3 +85,33 @@ def test_bf16_outputs_repeat_over_many_short_requests(bi, H, Hkv, Dh):
         differ += (c.run(bi, status=st) != first).sum()
     assert int(differ) == 0
     bi.check_status(st)
+
+
+# ---- calls on a stream of their own -----------------------------------------------------------------------------------
+
+def test_a_call_with_a_stream_keeps_its_memory_while_the_current_stream_works(bi):
+    """Blocks that the current stream has just let go, with writes to them still pending, and its allocations right
+    after the call: neither may meet the call's workspace or outputs."""
+    c = TreeCase([3000, 60, 500], [40, 12, 3], 32, 8, 128, 50)
+    x = normal((64, 50257), 51, 3.0, dtype=torch.float32).cuda()
+    tok = torch.randint(0, 50257, (64, 2), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    attend = lambda **kw: (c.run(bi, **kw),)
+    score = lambda **kw: bi.token_logprobs(x, tok, top_k=5, **kw)
+    sizes = [bi.tree_attention_workspace_size(3, 55, 32, 8, 128, c.max_nodes, c.max_seq),
+             bi.token_logprobs_workspace_size(64, 50257, 5), c.q.numel() * 2, 64 * 5 * 4]
+    want = [attend(), score()]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for call in (attend, score):
+            torch.cuda._sleep(200_000)
+            for n in sizes * 2:
+                torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+            got.append((call(stream=s), want[len(got) % 2]))
+            for n in sizes * 2:
+                torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.current_stream().wait_stream(s)
+    for outs, refs in got:
+        for a, b in zip(outs, refs):
+            assert same_bits(a, b)
