@@ -351,7 +351,10 @@ bi_status bi_embed(const bi_bf16* E, const int32_t* ids, bi_bf16* x, int32_t T, 
  * For token t of request r, its i-th: tok_req[t] = r, tok_pos[t] = pos0[r] +
  * depth[t] (depth: DEVICE [T] distance from the context, or NULL: i), and
  * slots[t] = 16 * page + offset of position pos0[r] + i (DEVICE [T] each).
- * Entries at or past the last token are left as they were.
+ * Entries at or past the last token are left as they were by bi_build_slots and
+ * become -1 in all three by bi_build_slots_padded: a step of a fixed T (one that
+ * is captured and replayed, say) needs the latter, since what an earlier step
+ * left there would be stored to as any other slot.
  * A request with a negative q_len adds no token.  A request whose positions do
  * not fit its row, or with a negative pos0, takes no page, and its tokens get
  * slot -1 (BI_DEV_BAD_POSITION); so does the first request that the free list
@@ -364,6 +367,11 @@ bi_status bi_build_slots(const int32_t* q_len, const int32_t* pos0, int32_t* pag
                          int32_t* free_head_out, const int32_t* depth, int32_t* cu_q, int32_t* tok_req,
                          int32_t* tok_pos, int32_t* slots, int32_t B, int32_t T, int32_t max_pages,
                          int32_t num_pages, int32_t* dev_status, bi_stream stream);
+bi_status bi_build_slots_padded(const int32_t* q_len, const int32_t* pos0, int32_t* page_table,
+                                const int32_t* free_pages, int32_t n_free, const int32_t* free_head,
+                                int32_t* free_head_out, const int32_t* depth, int32_t* cu_q, int32_t* tok_req,
+                                int32_t* tok_pos, int32_t* slots, int32_t B, int32_t T, int32_t max_pages,
+                                int32_t num_pages, int32_t* dev_status, bi_stream stream);
 
 /* bi_qk_norm_rope_append: per-head RMS norm of q and k, rotation and append to
  * the paged cache in one pass.  qkv: DEVICE [T, (H + 2*Hkv) * Dh] in qkv_dtype
@@ -377,7 +385,8 @@ bi_status bi_build_slots(const int32_t* q_len, const int32_t* pos0, int32_t* pag
  * results are bi_rope_kv_append's, bit for bit.
  * q goes to q_out (DEVICE [T, H, Dh]), k and v to slot slots[t] (16 * page +
  * offset, DEVICE [T]) of the caches (bi_rope_kv_append's layout); slot -1
- * stores neither (a padding token).  Two tokens may not share a slot.
+ * stores neither (a padding token; one at position -1 is not reported).  Two
+ * tokens may not share a slot.
  * A position outside 0..max_pos-1 leaves q unrotated and stores no k and v
  * (BI_DEV_BAD_POSITION); a slot outside the pool stores neither
  * (BI_DEV_BAD_PAGE).  Requires Dh % 16 == 0, Dh <= 256, 16-byte aligned qkv,

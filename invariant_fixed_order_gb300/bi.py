@@ -103,8 +103,8 @@ _proto("bi_log_softmax", _i32, _vp, _vp, _i32, _i32, _vp, _sz, _vp)
 _proto("bi_sample_workspace_size", _sz, _i32, _i32)
 _proto("bi_sample", _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _sz, _vp)
 _proto("bi_embed", _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp)
-_proto("bi_build_slots", _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
-       _vp, _vp)
+for _name in ("bi_build_slots", "bi_build_slots_padded"):
+    _proto(_name, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp)
 _proto("bi_qk_norm_rope_append", _i32, _vp, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32,
        _i32, _i32, _i32, _vp, _vp)
 _proto("bi_tree_attention_workspace_size", _sz, _i32, _i32, _i32, _i32, _i32, _i32, _i32)
@@ -504,14 +504,17 @@ def _args(*specs):
 
 
 def build_slots(q_len, pos0, page_table, free_pages, free_head, T: int, num_pages: int, depth=None, free_head_out=None,
-                cu_q=None, tok_req=None, tok_pos=None, slots=None, status=None, stream=None):
+                cu_q=None, tok_req=None, tok_pos=None, slots=None, status=None, stream=None, pad: bool | None = None):
     """Page tables and slot maps from request lengths, on the GPU.  Writes the new pages of each request into
     page_table and the first unused entry of free_pages into free_head_out (None: free_head itself).  T: rows of the
-    token arrays (at least the sum of q_len).  Returns (cu_q, tok_req, tok_pos, slots); tok_req and tok_pos may be
-    views of a step's metadata."""
+    token arrays (at least the sum of q_len).  pad: rows of the token arrays past the last token become -1 (padding for
+    qk_norm_rope_append); otherwise they are left as they were.  None: where this call makes one of the arrays.
+    Returns (cu_q, tok_req, tok_pos, slots); tok_req and tok_pos may be views of a step's metadata."""
     _shape(q_len, "q_len", None)
     B, dev = q_len.shape[0], q_len.device
     free_head_out = free_head if free_head_out is None else free_head_out
+    if pad is None:
+        pad = tok_req is None or tok_pos is None or slots is None
     cu_q = _result(stream, B + 1, dtype=torch.int32, device=dev) if cu_q is None else cu_q
     tok_req = _result(stream, T, dtype=torch.int32, device=dev) if tok_req is None else tok_req
     tok_pos = _result(stream, T, dtype=torch.int32, device=dev) if tok_pos is None else tok_pos
@@ -522,8 +525,9 @@ def build_slots(q_len, pos0, page_table, free_pages, free_head, T: int, num_page
         ("free_head", free_head, _I32, (1,), False), ("free_head_out", free_head_out, _I32, (1,), False),
         ("depth", depth, _I32, (T,), True), ("cu_q", cu_q, _I32, (B + 1,), False), ("tok_req", tok_req, _I32, (T,), False),
         ("tok_pos", tok_pos, _I32, (T,), False), ("slots", slots, _I32, (T,), False), ("status", status, _I32, None, True))
-    _check(_lib.bi_build_slots(q, p0, table, free, free_pages.shape[0], head, out, dep, cu, req, pos, slot, B, T,
-                               page_table.shape[1], num_pages, st, _stream(stream)))
+    call = _lib.bi_build_slots_padded if pad else _lib.bi_build_slots
+    _check(call(q, p0, table, free, free_pages.shape[0], head, out, dep, cu, req, pos, slot, B, T, page_table.shape[1],
+                num_pages, st, _stream(stream)))
     return cu_q, tok_req, tok_pos, slots
 
 

@@ -15,24 +15,44 @@ bool aligned16(const void* p) { return aligned(p, 16); }
 constexpr int32_t kMaxPages = 0x7fffffff / BI_PAGE;  // a slot (16 * page + offset) is an int32
 }  // namespace
 
+static bi_status run_build_slots(const char* name, bool pad, const int32_t* q_len, const int32_t* pos0,
+                                 int32_t* page_table, const int32_t* free_pages, int32_t n_free,
+                                 const int32_t* free_head, int32_t* free_head_out, const int32_t* depth, int32_t* cu_q,
+                                 int32_t* tok_req, int32_t* tok_pos, int32_t* slots, int32_t B, int32_t T,
+                                 int32_t max_pages, int32_t num_pages, int32_t* dev_status, bi_stream stream) {
+    const std::string n(name);
+    if (B < 0 || T < 0 || n_free < 0) return fail(BI_ERR_SHAPE, n + ": negative size");
+    if (max_pages <= 0 || num_pages <= 0 || max_pages > kMaxPages || num_pages > kMaxPages)
+        return fail(BI_ERR_SHAPE, n + ": need 0 < max_pages, num_pages < 2^27");
+    if (!free_head || !free_head_out || !cu_q || (n_free > 0 && !free_pages) || (B > 0 && (!q_len || !pos0 || !page_table)) ||
+        (T > 0 && (!tok_req || !tok_pos || !slots)))
+        return fail(BI_ERR_INVALID, n + ": null pointer");
+    const void* all[] = {q_len, pos0, page_table, free_pages, free_head, free_head_out, depth, cu_q, tok_req, tok_pos, slots};
+    for (const void* p : all)
+        if (!aligned(p, 4)) return fail(BI_ERR_INVALID, n + ": pointers must be 4-byte aligned");
+    cudaError_t e = launch_build_slots(q_len, pos0, page_table, free_pages, n_free, free_head, free_head_out, depth, cu_q,
+                                       tok_req, tok_pos, slots, pad, B, T, max_pages, num_pages, dev_status,
+                                       static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BI_OK : cuda_fail(e, (n + " launch").c_str());
+}
+
 extern "C" bi_status bi_build_slots(const int32_t* q_len, const int32_t* pos0, int32_t* page_table,
                                     const int32_t* free_pages, int32_t n_free, const int32_t* free_head,
                                     int32_t* free_head_out, const int32_t* depth, int32_t* cu_q, int32_t* tok_req,
                                     int32_t* tok_pos, int32_t* slots, int32_t B, int32_t T, int32_t max_pages,
                                     int32_t num_pages, int32_t* dev_status, bi_stream stream) {
-    if (B < 0 || T < 0 || n_free < 0) return fail(BI_ERR_SHAPE, "bi_build_slots: negative size");
-    if (max_pages <= 0 || num_pages <= 0 || max_pages > kMaxPages || num_pages > kMaxPages)
-        return fail(BI_ERR_SHAPE, "bi_build_slots: need 0 < max_pages, num_pages < 2^27");
-    if (!free_head || !free_head_out || !cu_q || (n_free > 0 && !free_pages) || (B > 0 && (!q_len || !pos0 || !page_table)) ||
-        (T > 0 && (!tok_req || !tok_pos || !slots)))
-        return fail(BI_ERR_INVALID, "bi_build_slots: null pointer");
-    const void* all[] = {q_len, pos0, page_table, free_pages, free_head, free_head_out, depth, cu_q, tok_req, tok_pos, slots};
-    for (const void* p : all)
-        if (!aligned(p, 4)) return fail(BI_ERR_INVALID, "bi_build_slots: pointers must be 4-byte aligned");
-    cudaError_t e = launch_build_slots(q_len, pos0, page_table, free_pages, n_free, free_head, free_head_out, depth, cu_q,
-                                       tok_req, tok_pos, slots, B, T, max_pages, num_pages, dev_status,
-                                       static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? BI_OK : cuda_fail(e, "bi_build_slots launch");
+    return run_build_slots("bi_build_slots", false, q_len, pos0, page_table, free_pages, n_free, free_head, free_head_out,
+                           depth, cu_q, tok_req, tok_pos, slots, B, T, max_pages, num_pages, dev_status, stream);
+}
+
+extern "C" bi_status bi_build_slots_padded(const int32_t* q_len, const int32_t* pos0, int32_t* page_table,
+                                           const int32_t* free_pages, int32_t n_free, const int32_t* free_head,
+                                           int32_t* free_head_out, const int32_t* depth, int32_t* cu_q, int32_t* tok_req,
+                                           int32_t* tok_pos, int32_t* slots, int32_t B, int32_t T, int32_t max_pages,
+                                           int32_t num_pages, int32_t* dev_status, bi_stream stream) {
+    return run_build_slots("bi_build_slots_padded", true, q_len, pos0, page_table, free_pages, n_free, free_head,
+                           free_head_out, depth, cu_q, tok_req, tok_pos, slots, B, T, max_pages, num_pages, dev_status,
+                           stream);
 }
 
 extern "C" bi_status bi_qk_norm_rope_append(const void* qkv, bi_dtype qkv_dtype, const bi_bf16* q_gamma,

@@ -157,7 +157,7 @@ cudaError_t launch_token_logprobs(const void* logits, bool f32, int64_t row_stri
 cudaError_t launch_build_slots(const int32_t* q_len, const int32_t* pos0, int32_t* page_table,
                                const int32_t* free_pages, int32_t n_free, const int32_t* free_head,
                                int32_t* free_head_out, const int32_t* depth, int32_t* cu_q, int32_t* tok_req,
-                               int32_t* tok_pos, int32_t* slots, int32_t B, int32_t T, int32_t max_pages,
+                               int32_t* tok_pos, int32_t* slots, bool pad, int32_t B, int32_t T, int32_t max_pages,
                                int32_t num_pages, int32_t* status, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_append(const void* qkv, bool f32, const bi_bf16* q_gamma, const bi_bf16* k_gamma,
                                        float eps, const int32_t* tok_pos, const int32_t* slots, const float* rc,

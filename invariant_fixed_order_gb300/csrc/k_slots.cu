@@ -28,7 +28,7 @@ constexpr int kSlotCluster = 8;
 struct SlotArgs {
     const int32_t *q_len, *pos0, *free_pages, *free_head, *depth;
     int32_t *page_table, *free_head_out, *cu_q, *tok_req, *tok_pos, *slots, *status;
-    int32_t B, T, max_pages, num_pages, n_free;
+    int32_t B, T, max_pages, num_pages, n_free, pad;
 };
 
 struct SlotSmem {
@@ -167,6 +167,10 @@ build_slots_kernel(SlotArgs a) {
         tok_base = tok_end;
         page_base = page_end;
     }
+    if (a.pad) {
+        const int64_t step = static_cast<int64_t>(ranks) * kSlotThreads;
+        for (int64_t t = tok_base + rank * kSlotThreads + tid; t < a.T; t += step) a.tok_req[t] = a.tok_pos[t] = a.slots[t] = -1;
+    }
     __syncthreads();
     if constexpr (kClustered) ptx::cluster_sync();  // every CTA has read free_head
     if (rank == 0 && tid == 0) {
@@ -178,10 +182,10 @@ build_slots_kernel(SlotArgs a) {
 cudaError_t launch_build_slots(const int32_t* q_len, const int32_t* pos0, int32_t* page_table,
                                const int32_t* free_pages, int32_t n_free, const int32_t* free_head,
                                int32_t* free_head_out, const int32_t* depth, int32_t* cu_q, int32_t* tok_req,
-                               int32_t* tok_pos, int32_t* slots, int32_t B, int32_t T, int32_t max_pages,
+                               int32_t* tok_pos, int32_t* slots, bool pad, int32_t B, int32_t T, int32_t max_pages,
                                int32_t num_pages, int32_t* status, cudaStream_t s) {
     const SlotArgs a{q_len, pos0, free_pages, free_head, depth, page_table, free_head_out, cu_q, tok_req, tok_pos,
-                     slots, status, B, T, max_pages, num_pages, n_free};
+                     slots, status, B, T, max_pages, num_pages, n_free, pad};
     // one CTA writes what a decode step needs in one sweep; more tokens than that are shared, by as many CTAs as have
     // a sweep of their own, or by a cluster where the list's head is updated in place
     if (T <= 4 * kSlotThreads || free_head_out != free_head) {
@@ -247,8 +251,8 @@ qk_norm_rope_append_kernel(QkArgs a) {
     const bool pos_ok = pos >= 0 && pos < a.max_pos;
     const bool slot_ok = slot >= 0 && slot / BI_PAGE < a.num_pages;
     if (threadIdx.x == 0 && blockIdx.y == 0) {
-        if (!pos_ok) report(a.status, BI_DEV_BAD_POSITION);
-        else if (!slot_ok && slot != -1) report(a.status, BI_DEV_BAD_PAGE);
+        if (!pos_ok && (pos != -1 || slot != -1)) report(a.status, BI_DEV_BAD_POSITION);
+        else if (pos_ok && !slot_ok && slot != -1) report(a.status, BI_DEV_BAD_PAGE);
     }
     float c[8], sn[8];
 #pragma unroll

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_tree import HEADS, INF, NAN, TREE_F32, TreeCase, close, normal, same_bits
+from test_gpu_tree import HEADS, INF, NAN, TREE_F32, TreeCase, close, i32, normal, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,83 @@ def test_a_call_with_a_stream_keeps_its_memory_while_the_current_stream_works(bi
     for outs, refs in got:
         for a, b in zip(outs, refs):
             assert same_bits(a, b)
+
+
+# ---- token rows behind the last token ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T", [64, 5000, 9000])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_rows_past_the_last_token_are_padding(bi, T, in_place):
+    q, p0 = [30, 0, 10], [3, 0, 0]
+    junk = [torch.full((T,), 3, dtype=torch.int32, device="cuda") for _ in range(64)]
+    del junk
+    args = lambda: (i32(q), i32(p0), i32(np.full((3, 4), 19)), i32(range(9)), i32([0]), T, 20)
+    out = None if in_place else i32([0])
+    got = bi.build_slots(*args(), free_head_out=out)
+    for x in got[1:]:
+        assert (x[40:] == -1).all() and (x[:40] >= 0).all()
+    # arrays of the caller's: left, unless asked for
+    mine = [torch.full((T,), 5, dtype=torch.int32, device="cuda") for _ in range(3)]
+    names = ("tok_req", "tok_pos", "slots")
+    bi.build_slots(*args(), free_head_out=out, **dict(zip(names, mine)))
+    for x, y in zip(mine, got[1:]):
+        assert (x[40:] == 5).all() and torch.equal(x[:40], y[:40])
+    bi.build_slots(*args(), free_head_out=out, pad=True, **dict(zip(names, mine)))
+    for x, y in zip(mine, got[1:]):
+        assert torch.equal(x, y)
+    # a row past T is nobody's; more tokens than rows leave none to pad
+    wide = [torch.full((T + 7,), 5, dtype=torch.int32, device="cuda") for _ in range(3)]
+    bi.build_slots(*args(), free_head_out=out, pad=True, **{n: w[:T] for n, w in zip(names, wide)})
+    assert all((w[T:] == 5).all() for w in wide)
+    st = bi.new_status()
+    a = args()
+    few = bi.build_slots(*a[:5], 35, 20, status=st)
+    assert int(st) == 0x202 and all(torch.equal(x, y[:35]) for x, y in zip(few[1:], got[1:]))
+
+
+def test_a_replayed_step_of_a_fixed_size_stores_its_own_tokens_only(bi):
+    """Slots and append captured for 48 tokens, replayed with fewer: what the earlier step stored stays."""
+    H, Hkv, Dh, T, pool = 4, 2, 64, 48, 20
+    qkv = normal((T, (H + 2 * Hkv) * Dh), 60, dtype=torch.float32).cuda()
+    k = torch.zeros(pool, Hkv, 16, Dh, dtype=torch.bfloat16, device="cuda")
+    v, q_out = torch.zeros_like(k), torch.zeros(T, H, Dh, dtype=torch.bfloat16, device="cuda")
+    c, s = (x.cuda() for x in bi.rope_table(64, Dh, 500000.0))
+    q_len, pos0, head, nxt, st = i32([40, 8]), i32([0, 0]), i32([0]), i32([0]), bi.new_status()
+    table, free = i32(np.full((2, 4), 19)), i32(range(12))
+
+    def step():
+        cu, req, pos, slots = bi.build_slots(q_len, pos0, table, free, head, T, pool, free_head_out=nxt, status=st)
+        bi.qk_norm_rope_append(qkv, None, None, pos, slots, c, s, q_out, k, v, H, Hkv, Dh, status=st)
+        return slots
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        slots = step()
+    g.replay()
+    bi.check_status(st)
+    first, k1, v1 = slots.clone(), k.clone(), v.clone()
+    assert (first >= 0).all()
+    qkv += 1.0
+    q_len.copy_(i32([3, 1])), pos0.copy_(i32([40, 8])), head.copy_(nxt)
+    g.replay()
+    bi.check_status(st)
+    assert (slots[:4] >= 0).all() and (slots[4:] == -1).all()
+    for now, was in ((k, k1), (v, v1)):
+        changed = (now != was).any(-1).any(1).nonzero()
+        assert sorted((changed[:, 0] * 16 + changed[:, 1]).tolist()) == sorted(slots[:4].tolist())
+
+
+def test_a_padding_token_is_not_reported_and_a_bad_position_is(bi):
+    H, Hkv, Dh = 4, 2, 64
+    qkv = normal((2, (H + 2 * Hkv) * Dh), 61).cuda()
+    c, s = (x.cuda() for x in bi.rope_table(64, Dh, 500000.0))
+    for pos, slot, code in ((-1, -1, 0), (5, -1, 0), (-2, -1, 0x202), (64, -1, 0x202), (-1, 4, 0x202), (5, -2, 0x201),
+                            (5, 48, 0x201)):
+        k = torch.zeros(3, Hkv, 16, Dh, dtype=torch.bfloat16, device="cuda")
+        v, st = torch.zeros_like(k), bi.new_status()
+        q_out = torch.zeros(2, H, Dh, dtype=torch.bfloat16, device="cuda")
+        bi.qk_norm_rope_append(qkv, None, None, i32([pos, 2]), i32([slot, 7]), c, s, q_out, k, v, H, Hkv, Dh, status=st)
+        assert int(st) == code, (pos, slot)
+        stored = (k != 0).any(-1).any(1).nonzero()
+        assert stored.tolist() == [[0, 7]]
