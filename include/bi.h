@@ -429,6 +429,23 @@ bi_status bi_tree_attention(const bi_bf16* q, const int32_t* cu_q, const int32_t
                             int32_t max_nodes, int32_t max_seq_len, float scale, void* ws, size_t ws_bytes,
                             int32_t* dev_status, bi_stream stream);
 
+/* bi_tree_attention's failure-detection check (for tests), as
+ * bi_gemm_wait_test: the waits of the warps that issue products give up after
+ * wait_limit_ns (1 ms to 2 s; the other roles leave as one of them does), and
+ * one copy of each CTA is never issued, skip_copy = 4 * item + 2 (where it is
+ * V's) + the copying warp (0 or 1): its half of the pages of K or V of the
+ * item-th step that the CTA walks (-1: none).  The wait for it runs out:
+ * the kernel writes BI_DEV_TIMEOUT_ATTENTION into dev_status (DEVICE, required),
+ * every role stops, the copies and products in flight are waited for, tensor
+ * memory is freed and the kernel returns; out holds no defined values. */
+bi_status bi_tree_attention_wait_test(const bi_bf16* q, const int32_t* cu_q, const int32_t* pos0,
+                                      const uint32_t* tree_mask, int32_t mask_words, const bi_bf16* k_cache,
+                                      const bi_bf16* v_cache, const int32_t* page_table, void* out,
+                                      bi_dtype out_dtype, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t Dh,
+                                      int32_t max_pages, int32_t num_pages, int32_t max_nodes, int32_t max_seq_len,
+                                      float scale, void* ws, size_t ws_bytes, uint64_t wait_limit_ns,
+                                      int32_t skip_copy, int32_t* dev_status, bi_stream stream);
+
 /* bi_token_logprobs: log probabilities of given tokens, entropy and the best
  * alternatives, without a [R, V] array.  logits: DEVICE [R, V] in
  * logits_dtype, rows row_stride elements apart (>= V).

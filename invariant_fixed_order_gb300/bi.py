@@ -110,6 +110,8 @@ _proto("bi_qk_norm_rope_append", _i32, _vp, _i32, _vp, _vp, _f32, _vp, _vp, _vp,
 _proto("bi_tree_attention_workspace_size", _sz, _i32, _i32, _i32, _i32, _i32, _i32, _i32)
 _proto("bi_tree_attention", _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
        _i32, _i32, _i32, _i32, _f32, _vp, _sz, _vp, _vp)
+_proto("bi_tree_attention_wait_test", _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+       _i32, _i32, _i32, _i32, _i32, _f32, _vp, _sz, ctypes.c_uint64, _i32, _vp, _vp)
 _proto("bi_token_logprobs_workspace_size", _sz, _i32, _i32, _i32)
 _proto("bi_token_logprobs", _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _sz, _vp, _vp)
 _proto("bi_model_create", _i32, ctypes.POINTER(ModelConfigC), ctypes.POINTER(ModelWeightsC),
@@ -557,7 +559,7 @@ def tree_attention_workspace_size(B: int, T: int, H: int, Hkv: int, Dh: int, max
 
 def tree_attention(q, cu_q, pos0, tree_mask, k_cache, v_cache, page_table, max_nodes: int,
                    max_seq_len: int | None = None, out_dtype: int = BF16, scale: float | None = None, ws=None,
-                   status=None, out=None, stream=None) -> torch.Tensor:
+                   status=None, out=None, stream=None, _wait_test=None) -> torch.Tensor:
     """Attention of drafted nodes over the paged cache.  tree_mask: int32 (or uint32) [T, words], bit j of a node's row
     set where it attends node j of its request (its own bit too); max_nodes: HOST bound on a request's nodes.
     max_seq_len None: the page table's capacity; scale None: the library's default."""
@@ -582,10 +584,17 @@ def tree_attention(q, cu_q, pos0, tree_mask, k_cache, v_cache, page_table, max_n
         ("v_cache", v_cache, _BF16, cache, False), ("page_table", page_table, _I32, None, False),
         ("out", out, _out_dt(out_dtype), (T, H, Dh), False), ("ws", ws, None, None, True),
         ("status", status, _I32, None, True))
-    _check(_lib.bi_tree_attention(pq, cu, p0, mask, tree_mask.shape[1], k, v, table, po, out_dtype, B, T, H, cache[1], Dh,
-                                  page_table.shape[1], cache[0], max_nodes, max_seq_len, 0.0 if scale is None else scale,
-                                  pw, 0 if ws is None else ws.numel() * ws.element_size(), st, _stream(stream)))
+    call, test = (_lib.bi_tree_attention, ()) if _wait_test is None else (_lib.bi_tree_attention_wait_test, _wait_test)
+    _check(call(pq, cu, p0, mask, tree_mask.shape[1], k, v, table, po, out_dtype, B, T, H, cache[1], Dh,
+                page_table.shape[1], cache[0], max_nodes, max_seq_len, 0.0 if scale is None else scale,
+                pw, 0 if ws is None else ws.numel() * ws.element_size(), *test, st, _stream(stream)))
     return out
+
+
+def tree_attention_wait_test(*args, status, wait_limit_ns: int = 1_000_000, skip_copy: int = 0, **kw) -> torch.Tensor:
+    """bi_tree_attention_wait_test: tree_attention with a short wait limit and one copy of each CTA withheld (its
+    bounded waits run out and the kernel reports through status)."""
+    return tree_attention(*args, status=status, _wait_test=(wait_limit_ns, skip_copy), **kw)
 
 
 def token_logprobs_workspace_size(R: int, V: int, K: int) -> int:

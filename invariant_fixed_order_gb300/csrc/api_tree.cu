@@ -87,12 +87,13 @@ extern "C" size_t bi_tree_attention_workspace_size(int32_t B, int32_t T, int32_t
     return tree_ws_bytes(B, T, H, Hkv, Dh, max_nodes, max_seq_len);
 }
 
-extern "C" bi_status bi_tree_attention(const bi_bf16* q, const int32_t* cu_q, const int32_t* pos0,
-                                       const uint32_t* tree_mask, int32_t mask_words, const bi_bf16* k_cache,
-                                       const bi_bf16* v_cache, const int32_t* page_table, void* out,
-                                       bi_dtype out_dtype, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t Dh,
-                                       int32_t max_pages, int32_t num_pages, int32_t max_nodes, int32_t max_seq_len,
-                                       float scale, void* ws, size_t ws_bytes, int32_t* dev_status, bi_stream stream) {
+static bi_status run_tree_attention(const bi_bf16* q, const int32_t* cu_q, const int32_t* pos0,
+                                    const uint32_t* tree_mask, int32_t mask_words, const bi_bf16* k_cache,
+                                    const bi_bf16* v_cache, const int32_t* page_table, void* out,
+                                    bi_dtype out_dtype, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t Dh,
+                                    int32_t max_pages, int32_t num_pages, int32_t max_nodes, int32_t max_seq_len,
+                                    float scale, void* ws, size_t ws_bytes, int32_t* dev_status, bi_stream stream,
+                                    uint64_t wait_ns, int32_t skip_copy) {
     if (B < 0 || T < 0) return fail(BI_ERR_SHAPE, "bi_tree_attention: negative size");
     if (!attention_supported(H, Hkv, Dh))
         return fail(BI_ERR_UNSUPPORTED, "bi_tree_attention: need Dh in {64,128} and H/Hkv in {1,2,4,8}");
@@ -114,9 +115,37 @@ extern "C" bi_status bi_tree_attention(const bi_bf16* q, const int32_t* cu_q, co
     if (need > 0 && (!ws || ws_bytes < need)) return fail(BI_ERR_WORKSPACE, "bi_tree_attention: workspace too small");
     if (!aligned16(ws)) return fail(BI_ERR_INVALID, "bi_tree_attention: workspace must be 16-byte aligned");
     const TreeArgs a{q, k_cache, v_cache, cu_q, pos0, page_table, tree_mask, out, out_dtype == BI_F32, mask_words, B, T,
-                     H, Hkv, Dh, max_pages, num_pages, max_nodes, max_seq_len, default_scale(scale, Dh), dev_status};
+                     H, Hkv, Dh, max_pages, num_pages, max_nodes, max_seq_len, default_scale(scale, Dh), dev_status,
+                     wait_ns, skip_copy};
     cudaError_t e = launch_tree_attention(a, ws, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? BI_OK : cuda_fail(e, "bi_tree_attention launch");
+}
+
+extern "C" bi_status bi_tree_attention(const bi_bf16* q, const int32_t* cu_q, const int32_t* pos0,
+                                       const uint32_t* tree_mask, int32_t mask_words, const bi_bf16* k_cache,
+                                       const bi_bf16* v_cache, const int32_t* page_table, void* out,
+                                       bi_dtype out_dtype, int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t Dh,
+                                       int32_t max_pages, int32_t num_pages, int32_t max_nodes, int32_t max_seq_len,
+                                       float scale, void* ws, size_t ws_bytes, int32_t* dev_status, bi_stream stream) {
+    return run_tree_attention(q, cu_q, pos0, tree_mask, mask_words, k_cache, v_cache, page_table, out, out_dtype, B, T, H,
+                              Hkv, Dh, max_pages, num_pages, max_nodes, max_seq_len, scale, ws, ws_bytes, dev_status,
+                              stream, kWaitLimitNs, -1);
+}
+
+extern "C" bi_status bi_tree_attention_wait_test(const bi_bf16* q, const int32_t* cu_q, const int32_t* pos0,
+                                                 const uint32_t* tree_mask, int32_t mask_words, const bi_bf16* k_cache,
+                                                 const bi_bf16* v_cache, const int32_t* page_table, void* out,
+                                                 bi_dtype out_dtype, int32_t B, int32_t T, int32_t H, int32_t Hkv,
+                                                 int32_t Dh, int32_t max_pages, int32_t num_pages, int32_t max_nodes,
+                                                 int32_t max_seq_len, float scale, void* ws, size_t ws_bytes,
+                                                 uint64_t wait_limit_ns, int32_t skip_copy, int32_t* dev_status,
+                                                 bi_stream stream) {
+    if (!dev_status) return fail(BI_ERR_INVALID, "bi_tree_attention_wait_test: needs dev_status");
+    if (wait_limit_ns < 1000000ull || wait_limit_ns > kWaitLimitNs)
+        return fail(BI_ERR_INVALID, "bi_tree_attention_wait_test: wait limit outside [1 ms, 2 s]");
+    return run_tree_attention(q, cu_q, pos0, tree_mask, mask_words, k_cache, v_cache, page_table, out, out_dtype, B, T, H,
+                              Hkv, Dh, max_pages, num_pages, max_nodes, max_seq_len, scale, ws, ws_bytes, dev_status,
+                              stream, wait_limit_ns, skip_copy);
 }
 
 extern "C" size_t bi_token_logprobs_workspace_size(int32_t R, int32_t V, int32_t K) {

@@ -172,6 +172,8 @@ struct TreeArgs {
     int32_t out_f32, words, B, T, H, Hkv, Dh, max_pages, num_pages, max_nodes, max_seq;
     float scale;
     int32_t* status;
+    uint64_t wait_ns;        // limit of the issuing warps' waits
+    int32_t skip_copy;       // wait test: the copy that is withheld (4 * item + 2 for V + copying warp), else -1
 };
 size_t tree_ws_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t Dh, int32_t max_nodes, int32_t max_seq);
 cudaError_t launch_tree_attention(const TreeArgs& a, void* ws, cudaStream_t s);

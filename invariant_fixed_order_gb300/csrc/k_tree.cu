@@ -119,7 +119,7 @@ struct Smem {
     uint64_t run_full[2][2];                   // P of a run's last half step written
     uint64_t rd_full[2], rd_free[2];
     uint64_t drain[2];
-    uint32_t k_issued[kStagesK], v_issued[kStagesV], q_issued[2];  // fills so far
+    uint32_t k_issued[2][kStagesK], v_issued[2][kStagesV], q_issued[2];  // fills so far (by copying warp)
     uint32_t tmem_base;
     int32_t abort;
     uint32_t bad[2][BI_TREE_MAX_NODES / 32];   // nodes whose V is not finite, by run parity
@@ -227,7 +227,7 @@ __device__ __forceinline__ uint32_t visible(const uint32_t* mask, int32_t kb, in
 // order of use, K two items ahead of V, on from one run to the next.
 // ---------------------------------------------------------------------------
 
-template <int G, int DH, bool kFirst>
+template <int G, int DH, bool kFirst, bool kTest>
 __device__ __forceinline__ void produce(Smem<DH>& sm, const CUtensorMap* tmK, const CUtensorMap* tmV,
                                         const CUtensorMap* tmQ, const TreeArgs& a, int32_t slots) {
     constexpr int NT = kRows / G;
@@ -250,10 +250,11 @@ __device__ __forceinline__ void produce(Smem<DH>& sm, const CUtensorMap* tmK, co
         int32_t y, np;
     };
     Copy late0{0, 0}, late1{0, 0};  // the items whose V is still to be copied: of even and odd place in the CTA
-    constexpr int kPages = kStepPages / 2, kFrom = kFirst ? 0 : kPages;
+    constexpr int kWarp = kFirst ? 0 : 1, kPages = kStepPages / 2, kFrom = kWarp * kPages;
+    auto withheld = [&](uint32_t at, int v) { return kTest && a.skip_copy == static_cast<int32_t>(4 * at) + 2 * v + kWarp; };
     auto arm = [&](uint64_t* full, int32_t np, uint32_t* issued, uint32_t fills) {
         if (lane == 0) {
-            if (kFirst) *issued = fills;
+            *issued = fills;
             ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(np * kRegions * BI_PAGE * 128));
         }
         __syncwarp();
@@ -261,7 +262,8 @@ __device__ __forceinline__ void produce(Smem<DH>& sm, const CUtensorMap* tmK, co
     auto copy_k = [&](uint32_t at, const Copy& c) {
         const uint32_t st = at % kStagesK;
         if (at >= kStagesK && !wait(&sm.k_free[st], (at / kStagesK - 1) & 1u)) return false;
-        arm(&sm.k_full[st], c.np, &sm.k_issued[st], at / kStagesK + 1);
+        if (withheld(at, 0)) return true;
+        arm(&sm.k_full[st], c.np, &sm.k_issued[kWarp][st], at / kStagesK + 1);
         const int h = lane / kPages, x = lane & (kPages - 1);
         if (h < kRegions && x < c.np)
             ptx::tma_load_2d(&sm.k[st][h * kRegion + (kFrom + x) * (BI_PAGE * 128)], tmK, &sm.k_full[st], h * 64, c.y);
@@ -271,7 +273,8 @@ __device__ __forceinline__ void produce(Smem<DH>& sm, const CUtensorMap* tmK, co
     auto copy_v = [&](uint32_t at, const Copy& c) {
         const uint32_t st = at % kStagesV;
         if (at >= kStagesV && !wait(&sm.v_free[st], (at / kStagesV - 1) & 1u)) return false;
-        arm(&sm.v_full[st], c.np, &sm.v_issued[st], at / kStagesV + 1);
+        if (withheld(at, 1)) return true;
+        arm(&sm.v_full[st], c.np, &sm.v_issued[kWarp][st], at / kStagesV + 1);
         if (lane < c.np)
             ptx::tma_load_3d(&sm.v[st][(kFrom + lane) * (kRegions * BI_PAGE * 128)], tmV, &sm.v_full[st], 0, c.y, 0, policy);
         __syncwarp();
@@ -533,8 +536,8 @@ __device__ __forceinline__ void commit_elected(uint64_t* bar) {
 // the scores take the buffer whose P was multiplied just before them, in order.
 // Every stage of K and V is waited for and let go by both lanes, in turn, so
 // that none can take one fill's phase for another's.
-template <int DH>
-__device__ __forceinline__ void issue_products(Smem<DH>& sm, uint32_t tmem, int lane_id) {
+template <int DH, bool kTest>
+__device__ __forceinline__ void issue_products(Smem<DH>& sm, uint32_t tmem, int lane_id, uint64_t wait_ns) {
     constexpr int kStagesK = Smem<DH>::kStagesK, kStagesV = Smem<DH>::kStagesV;
     constexpr uint32_t kUnit = 16;  // a descriptor's address field counts 16 bytes: steps of an operand are added to it
     const uint32_t idesc_s = ptx::idesc_bf16_f32(kRows, kHalf);
@@ -547,7 +550,7 @@ __device__ __forceinline__ void issue_products(Smem<DH>& sm, uint32_t tmem, int 
     uint32_t runs = 0, mine = 0, halves = 0, fills = 0, base = 0;
     uint32_t next_k = 0, next_v = 0;                    // items of K and V seen
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, abort); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity, abort, kTest ? wait_ns : kWaitLimitNs); };
     auto same = [](int32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
     // waits for item `to`; the ones before it are the other lane's
     auto see_k = [&](uint32_t to, bool own) {
@@ -880,12 +883,14 @@ __device__ __forceinline__ void consume(Smem<DH>& sm, uint32_t tmem, const TreeA
         }
     };
     if (!walk()) {
+        tmem_st_wait();  // (tensor memory is freed next)
         if (lane == 0) report(a.status, BI_DEV_TIMEOUT_ATTENTION);
         *abort = 1;  // the other roles' waits give up at once
     }
 }
 
-template <int G, int DH>
+// kTest: bi_tree_attention_wait_test's form (the tests cost the other 1 to 2 %)
+template <int G, int DH, bool kTest>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, TreeArgs a, Layout lay) {
@@ -899,12 +904,12 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         ptx::prefetch_tmap(&tmV);
         ptx::prefetch_tmap(&tmQ);
         for (int s = 0; s < Smem<DH>::kStagesK; ++s) {
-            sm.k_issued[s] = 0;
+            sm.k_issued[0][s] = sm.k_issued[1][s] = 0;
             ptx::mbar_init(&sm.k_full[s], 2);  // the copying warps
             ptx::mbar_init(&sm.k_free[s], 2);  // the lanes
         }
         for (int s = 0; s < Smem<DH>::kStagesV; ++s) {
-            sm.v_issued[s] = 0;
+            sm.v_issued[0][s] = sm.v_issued[1][s] = 0;
             ptx::mbar_init(&sm.v_full[s], 2);
             ptx::mbar_init(&sm.v_free[s], 2);
         }
@@ -937,9 +942,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     pdl_wait();
     const uint32_t tmem = sm.tmem_base;
     if (warp >= kSoftWarps) {
-        if (warp == kSoftWarps) produce<G, DH, true>(sm, &tmK, &tmV, &tmQ, a, lay.slots);
-        else if (warp == kSoftWarps + 2) produce<G, DH, false>(sm, &tmK, &tmV, nullptr, a, lay.slots);
-        else issue_products<DH>(sm, tmem, warp == kSoftWarps + 1 ? 0 : 1);
+        if (warp == kSoftWarps) produce<G, DH, true, kTest>(sm, &tmK, &tmV, &tmQ, a, lay.slots);
+        else if (warp == kSoftWarps + 2) produce<G, DH, false, kTest>(sm, &tmK, &tmV, nullptr, a, lay.slots);
+        else issue_products<DH, kTest>(sm, tmem, warp == kSoftWarps + 1 ? 0 : 1, a.wait_ns);
     } else {
         consume<G, DH>(sm, tmem, a, lay);
     }
@@ -949,13 +954,18 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     if (warp == 0) {
         ptx::tmem_dealloc<1>(tmem, kTmemCols);
         if (sm.abort && lane == 0) {
-            // every copy issued has landed before the shared memory is released (the issuing warp, had it not
-            // stopped, would have waited for each)
+            // Every copy issued has landed before the shared memory is released (the issuing warps, had they not
+            // stopped, would have waited for each).  A stage is filled anew only once both copying warps have
+            // armed it and its fill was seen, so their counts differ by one at most: there the arrival of the warp
+            // that stopped is made up for, so that the phase ends with the other's copies.
             volatile int32_t none = 0;
-            for (int st = 0; st < Smem<DH>::kStagesK; ++st)
-                if (sm.k_issued[st]) ptx::mbar_wait_bounded(&sm.k_full[st], (sm.k_issued[st] - 1) & 1u, &none);
-            for (int st = 0; st < Smem<DH>::kStagesV; ++st)
-                if (sm.v_issued[st]) ptx::mbar_wait_bounded(&sm.v_full[st], (sm.v_issued[st] - 1) & 1u, &none);
+            auto landed = [&](uint64_t* full, uint32_t first, uint32_t second) {
+                const uint32_t fills = max(first, second);
+                if (first != second) mbar_arrive(full);
+                if (fills > 0) ptx::mbar_wait_bounded(full, (fills - 1) & 1u, &none);
+            };
+            for (int st = 0; st < Smem<DH>::kStagesK; ++st) landed(&sm.k_full[st], sm.k_issued[0][st], sm.k_issued[1][st]);
+            for (int st = 0; st < Smem<DH>::kStagesV; ++st) landed(&sm.v_full[st], sm.v_issued[0][st], sm.v_issued[1][st]);
             for (int st = 0; st < 2; ++st)
                 if (sm.q_issued[st]) ptx::mbar_wait_bounded(&sm.q_full[st], (sm.q_issued[st] - 1) & 1u, &none);
         }
@@ -1063,7 +1073,7 @@ static int32_t launch_rows(int32_t max_nodes, int32_t G) {
 static size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 static int32_t launch_slots(int32_t max_seq, int32_t Hkv) { return most_segments((max_seq - 1) / kStep + 1, Hkv); }
 
-template <int G, int DH>
+template <int G, int DH, bool kTest>
 cudaError_t launch_kernel(const TreeArgs& a, const Layout& lay, unsigned ctas, const CUtensorMap& tmK,
                           const CUtensorMap& tmV, const CUtensorMap& tmQ, cudaStream_t s) {
     const size_t smem = sizeof(Smem<DH>);
@@ -1071,11 +1081,11 @@ cudaError_t launch_kernel(const TreeArgs& a, const Layout& lay, unsigned ctas, c
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [smem] {
-        attr_err = cudaFuncSetAttribute(tree_attention_kernel<G, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr_err = cudaFuncSetAttribute(tree_attention_kernel<G, DH, kTest>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(smem));
     });
     if (attr_err != cudaSuccess) return attr_err;
-    return launch_pdl(tree_attention_kernel<G, DH>, dim3(ctas), dim3(kThreads), smem, s, tmK, tmV, tmQ, a, lay);
+    return launch_pdl(tree_attention_kernel<G, DH, kTest>, dim3(ctas), dim3(kThreads), smem, s, tmK, tmV, tmQ, a, lay);
 }
 
 template <int G, int DH>
@@ -1091,7 +1101,8 @@ cudaError_t launch(const TreeArgs& a, void* ws, cudaStream_t s) {
     char* w = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(ws)));
     lay.ml = reinterpret_cast<float2*>(w);
     lay.o = reinterpret_cast<float4*>(w + align_up(static_cast<size_t>(tiles) * slots * lay.rows * sizeof(float2)));
-    const cudaError_t e = launch_kernel<G, DH>(a, lay, ctas, tmK, tmV, tmQ, s);
+    const cudaError_t e = a.wait_ns == kWaitLimitNs && a.skip_copy < 0 ? launch_kernel<G, DH, false>(a, lay, ctas, tmK, tmV, tmQ, s)
+                                                                       : launch_kernel<G, DH, true>(a, lay, ctas, tmK, tmV, tmQ, s);
     if (e != cudaSuccess) return e;
     // one block for all dims of its rows, or, while that leaves SMs without one, a block for each 32
     const bool few = tiles * (lay.rows / kMergeRows) < 4 * num_sms();

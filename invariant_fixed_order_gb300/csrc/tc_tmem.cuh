@@ -26,14 +26,16 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // kHintNs (it resumes when the phase completes), so waiting warps take few
 // issue slots from the softmax warps that share their schedulers.
 constexpr uint32_t kHintNs = 20000;
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int32_t* abort) {
-    return ptx::mbar_wait_bounded_hint(bar, parity, abort, kHintNs);
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int32_t* abort,
+                                             uint64_t limit_ns = kWaitLimitNs) {
+    return ptx::mbar_wait_bounded_hint(bar, parity, abort, kHintNs, limit_ns);
 }
 // Every thread of a warp: a bounded wait whose outcome is the same in the
 // whole warp (a failure in one lane fails the warp), so the warp-collective
 // tensor-memory accesses that follow stay uniform.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort) {
-    return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort,
+                                          uint64_t limit_ns = kWaitLimitNs) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort, limit_ns));
 }
 
 // Byte offset of 16-byte chunk c (0..7) of row r in a 128-byte-swizzled region.

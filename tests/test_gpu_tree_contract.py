@@ -195,3 +195,37 @@ def test_a_padding_token_is_not_reported_and_a_bad_position_is(bi):
         assert int(st) == code, (pos, slot)
         stored = (k != 0).any(-1).any(1).nonzero()
         assert stored.tolist() == [[0, 7]]
+
+
+# ---- a wait that runs out ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,Hkv,Dh", [(32, 8, 128), (8, 1, 64)])
+@pytest.mark.parametrize("item", [0, 1, 2, 4, 6])
+@pytest.mark.parametrize("v", [0, 1])
+@pytest.mark.parametrize("warp", [0, 1])
+def test_a_wait_that_runs_out_is_reported_and_the_stream_recovers(bi, H, Hkv, Dh, item, v, warp):
+    """Failure detection without a fault: one copy of K or V is withheld in every CTA, by either copying warp, so the
+    waits for it give up after 2 ms; the kernel reports a timeout, waits for the copies and products in flight, frees
+    tensor memory and returns.  Calls right after it, on the same memory, are right.  Pairs of tiles, odd ones and lone
+    requests over enough steps that later fills of a stage are withheld too."""
+    c = TreeCase([9000, 300, 12000, 5], [70, 5, 20, 100], H, Hkv, Dh, 70)
+    want = c.run(bi, out_dtype=bi.F32).clone()
+    st, st2 = bi.new_status(), bi.new_status()
+    ws = torch.empty(bi.tree_attention_workspace_size(4, 195, H, Hkv, Dh, c.max_nodes, c.max_seq), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.empty_like(want)
+    bi.tree_attention_wait_test(c.q, c.cu, c.pos0, c.mask, c.k, c.v, c.table, c.max_nodes, max_seq_len=c.max_seq,
+                                out_dtype=bi.F32, ws=ws, out=out, status=st, wait_limit_ns=2_000_000,
+                                skip_copy=4 * item + 2 * v + warp)
+    again = [c.run(bi, out_dtype=bi.F32, ws=ws, status=st2).clone() for _ in range(3)]
+    with pytest.raises(bi.BIError) as e:
+        bi.check_status(st)
+    assert e.value.status == bi.BI_ERR_TIMEOUT
+    bi.check_status(st2)
+    assert all(same_bits(x, want) for x in again)
+    # nothing withheld: an ordinary call within the limit
+    bi.reset_status(st)
+    bi.tree_attention_wait_test(c.q, c.cu, c.pos0, c.mask, c.k, c.v, c.table, c.max_nodes, max_seq_len=c.max_seq,
+                                out_dtype=bi.F32, ws=ws, out=out, status=st, wait_limit_ns=100_000_000, skip_copy=-1)
+    bi.check_status(st)
+    assert same_bits(out, want)
