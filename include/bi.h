@@ -411,10 +411,13 @@ bi_status bi_qk_norm_rope_append(const void* qkv, bi_dtype qkv_dtype, const bi_b
  * holds there (NaN and infinities included).
  * Arithmetic: scores in fp32 (bf16 products), softmax statistics and sums in
  * fp32; the weights p = 2^(score - reference) multiply V as bf16 hi + lo parts;
- * a bf16 output is the fp32 output, rounded once.  A request's positions are cut into at most BI_TREE_MAX_SEGMENTS segments of whole 128
- * positions, walked 64 at a time, whose results are folded in ascending order;
- * the cut follows from its positions, nodes, H and Hkv, so a row's bits are its
- * request's.
+ * a bf16 output is the fp32 output, rounded once.  A request's positions are
+ * cut into segments of bi_tree_attention_segment positions (whole 128s, at most
+ * BI_TREE_MAX_SEGMENTS of them), walked 64 at a time, whose results are folded
+ * in ascending order.  The cut follows from the request's positions and nodes, H
+ * and Hkv, so a row's bits are its request's; they may change with the size of
+ * its draft, and are not those of bi_decode_attention or bi_prefill_attention
+ * over the same keys (a chain gets their values, not their bits).
  * max_seq_len: HOST bound on pos0[r] + nodes (0 < max_seq_len <= max_pages *
  * 16); a request outside its bounds gets zeros (BI_DEV_BAD_POSITION).
  * ws: DEVICE scratch of bi_tree_attention_workspace_size bytes, 16-byte
@@ -422,6 +425,9 @@ bi_status bi_qk_norm_rope_append(const void* qkv, bi_dtype qkv_dtype, const bi_b
  * (or NaN) selects the default, as in bi_decode_attention. */
 size_t bi_tree_attention_workspace_size(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t Dh, int32_t max_nodes,
                                         int32_t max_seq_len);
+/* Positions of a segment of a request with so many positions (context and
+ * nodes), or 0 for arguments that bi_tree_attention does not take. */
+int32_t bi_tree_attention_segment(int32_t positions, int32_t nodes, int32_t H, int32_t Hkv);
 bi_status bi_tree_attention(const bi_bf16* q, const int32_t* cu_q, const int32_t* pos0, const uint32_t* tree_mask,
                             int32_t mask_words, const bi_bf16* k_cache, const bi_bf16* v_cache,
                             const int32_t* page_table, void* out, bi_dtype out_dtype, int32_t B, int32_t T,

@@ -108,6 +108,7 @@ for _name in ("bi_build_slots", "bi_build_slots_padded"):
 _proto("bi_qk_norm_rope_append", _i32, _vp, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32,
        _i32, _i32, _i32, _vp, _vp)
 _proto("bi_tree_attention_workspace_size", _sz, _i32, _i32, _i32, _i32, _i32, _i32, _i32)
+_proto("bi_tree_attention_segment", _i32, _i32, _i32, _i32, _i32)
 _proto("bi_tree_attention", _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
        _i32, _i32, _i32, _i32, _f32, _vp, _sz, _vp, _vp)
 _proto("bi_tree_attention_wait_test", _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
@@ -555,6 +556,11 @@ def qk_norm_rope_append(qkv, q_gamma, k_gamma, tok_pos, slots, rope_cos, rope_si
 
 def tree_attention_workspace_size(B: int, T: int, H: int, Hkv: int, Dh: int, max_nodes: int, max_seq_len: int) -> int:
     return int(_lib.bi_tree_attention_workspace_size(B, T, H, Hkv, Dh, max_nodes, max_seq_len))
+
+
+def tree_attention_segment(positions: int, nodes: int, H: int, Hkv: int) -> int:
+    """Positions per segment that a request's keys are cut into (0: not supported)."""
+    return int(_lib.bi_tree_attention_segment(positions, nodes, H, Hkv))
 
 
 def tree_attention(q, cu_q, pos0, tree_mask, k_cache, v_cache, page_table, max_nodes: int,

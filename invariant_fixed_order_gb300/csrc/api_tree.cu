@@ -87,6 +87,13 @@ extern "C" size_t bi_tree_attention_workspace_size(int32_t B, int32_t T, int32_t
     return tree_ws_bytes(B, T, H, Hkv, Dh, max_nodes, max_seq_len);
 }
 
+extern "C" int32_t bi_tree_attention_segment(int32_t positions, int32_t nodes, int32_t H, int32_t Hkv) {
+    if (positions <= 0 || positions > 0x7fffff00 || nodes <= 0 || nodes > BI_TREE_MAX_NODES || nodes > positions ||
+        !attention_supported(H, Hkv, 128))
+        return 0;
+    return tree_segment(positions, nodes, H, Hkv);
+}
+
 static bi_status run_tree_attention(const bi_bf16* q, const int32_t* cu_q, const int32_t* pos0,
                                     const uint32_t* tree_mask, int32_t mask_words, const bi_bf16* k_cache,
                                     const bi_bf16* v_cache, const int32_t* page_table, void* out,

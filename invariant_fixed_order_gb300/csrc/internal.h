@@ -175,6 +175,7 @@ struct TreeArgs {
     uint64_t wait_ns;        // limit of the issuing warps' waits
     int32_t skip_copy;       // wait test: the copy that is withheld (4 * item + 2 for V + copying warp), else -1
 };
+int32_t tree_segment(int32_t positions, int32_t nodes, int32_t H, int32_t Hkv);
 size_t tree_ws_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t Dh, int32_t max_nodes, int32_t max_seq);
 cudaError_t launch_tree_attention(const TreeArgs& a, void* ws, cudaStream_t s);
 

@@ -149,29 +149,48 @@ __device__ __forceinline__ float max_of(const uint32_t (&s)[N]) {
     return max3(fmaxf(m[0], m[1]), m[2], m[3]);
 }
 
-// Steps per segment of a request of so many steps whose rows make `tiles`
-// tiles over all KV heads.  Segments spread a lone request over the CTAs, and
-// each costs a full batch a partial of its tile written and read (66 KB at
-// most, a step's K and V are 64 KB) and its CTA a change of run: short ones for
-// short contexts, twice as long where pairs of tiles halve the keys' traffic
-// (tiles >= 16), at most 16 for a request that fills CTAs with its tiles, 32
-// for one of few tiles.  Measured, one request of 6 steps / 16 requests / 64
-// with pairs / two of 240 steps on few tiles, us: 1 step up to 8, else this
-// 10.7 / 76.2 / 339 / 44; 4 steps everywhere 10.8 / 79 / 388 / 44; 8 (pairs
-// too) 11.3 / 84 / 388 / 45; this with 8 for 10 11.1 / 75.1 / 326 / 44, with 12
-// for 10 11.1 / 76.6 / 326 / 40, with 24 for 16 11.1 / 75.5 / 322 / 44; this
-// 11.1 / 72.8 / 326 / 30.5 (the last one's runs are no more than the SMs).
-__device__ __forceinline__ int32_t segment_steps(int32_t steps, int32_t tiles) {
-    int32_t s = steps <= 8 ? (tiles >= 16 ? 4 : 2) : steps <= 16 ? 4 : tiles >= 16 ? 16 : 10;
-    const int32_t most = tiles >= 8 ? BI_TREE_MAX_SEGMENTS / 2 : BI_TREE_MAX_SEGMENTS;
-    while ((steps + s - 1) / s > most) s *= 2;
-    return s;
+// Steps per segment of a request of so many steps whose rows make `tiles` tiles
+// over all KV heads.  A segment costs a partial of each of its tiles, written
+// and read (66 KB at most; a step's K and V are 64 KB), and a change of run;
+// what it gives is CTAs for a request with few of its own.  So a request is cut
+// into about kSegRuns pieces (tiles x segments), a segment is at least 2 steps,
+// and no more than kSegLong, or kSegPairs where there are tiles enough to share
+// their keys in pairs: longer ones spread a batch unevenly.  The number of
+// segments is bounded, which bounds the workspace.
+// Measured, us, means over 60 random sets of lengths of each kind: lone requests
+// of 150 to 32000 positions with 8 tiles, 16 tiles, 2 KV heads / 2 to 4 requests of
+// 8000 to 32000 with 2 KV heads, 2 to 6 of 4000 to 32000 with 8 / 16 and 64 requests
+// of up to 8192 with 8 tiles, 64 with 16:
+//   as below        19.3 28.7 23.1 / 47.3 81.2 / 80.9 248 373
+//   kSegLong 7      18.2 28.7 21.1 / 47.4 82.3 / 80.4 255 371
+//   kSegLong 8      18.5 28.7 21.8 / 47.5 82.3 / 80.1 252 372
+//   kSegLong 11     19.6 28.7 23.7 / 46.3 81.6 / 81.4 248 374
+//   kSegRuns 40     18.8 27.6 22.7 / 47.5 81.5 / 82.0 256 386
+//   kSegPairs 20    19.2 31.0 23.1 / 47.3 81.2 / 80.9 248 371
+// and over 30 sets, against the like: kSegRuns 24 1 to 6 % longer for lone requests
+// and 1 to 2 % for batches; kSegShort 1 within 2 %; kSegPairs 8 13 % shorter for a
+// lone request of 16 tiles, 10 % longer for 64.  From 7 to 11 kSegLong trades lone
+// requests for batches, a few percent either way.
+constexpr int32_t kSegRuns = 32, kSegShort = 2, kSegLong = 10, kSegPairs = 16, kPairTiles = 16, kFewTiles = 8;
+__host__ __device__ constexpr int32_t segments_bound(int32_t tiles) {
+    return tiles >= kFewTiles ? BI_TREE_MAX_SEGMENTS / 2 : BI_TREE_MAX_SEGMENTS;
 }
-// The most segments that a request of up to so many steps has (it has a tile for each KV head at least).
+__host__ __device__ constexpr int32_t longest_segment(int32_t tiles) { return tiles >= kPairTiles ? kSegPairs : kSegLong; }
+__host__ __device__ constexpr int32_t segment_steps(int32_t steps, int32_t tiles) {
+    const int64_t even = (static_cast<int64_t>(steps) * tiles + kSegRuns - 1) / kSegRuns;
+    const int32_t most = longest_segment(tiles), least = (steps + segments_bound(tiles) - 1) / segments_bound(tiles);
+    const int32_t s = even < kSegShort ? kSegShort : even > most ? most : static_cast<int32_t>(even);
+    return s > least ? s : least;
+}
+// The most segments that a request of up to so many steps has.  It has a tile for
+// each KV head at least, and fewer segments with more tiles; of s steps each they
+// are ceil(steps / s), where s >= 2 and either s >= steps tiles / kSegRuns or s is
+// the longest.
 static int32_t most_segments(int32_t steps, int32_t Hkv) {
-    const int32_t most = Hkv >= 8 ? BI_TREE_MAX_SEGMENTS / 2 : BI_TREE_MAX_SEGMENTS;
-    const int32_t n = steps <= 16 ? (steps + 1) / 2 : (steps + 7) / 8 > 8 ? (steps + 7) / 8 : 8;
-    return n < most ? n : most;
+    const int32_t runs = (kSegRuns + Hkv - 1) / Hkv, full = (steps + longest_segment(Hkv) - 1) / longest_segment(Hkv);
+    const int32_t n = runs > full ? runs : full, shortest = (steps + kSegShort - 1) / kSegShort;
+    const int32_t m = n < shortest ? n : shortest;
+    return m < segments_bound(Hkv) ? m : segments_bound(Hkv);
 }
 
 // Work of a run, in steps of K and V: its own, and what the change of queries,
@@ -1111,6 +1130,11 @@ cudaError_t launch(const TreeArgs& a, void* ws, cudaStream_t s) {
 }
 
 }  // namespace tree
+
+int32_t tree_segment(int32_t positions, int32_t nodes, int32_t H, int32_t Hkv) {
+    const int32_t NT = tree::kRows / (H / Hkv), steps = (positions + tree::kStep - 1) / tree::kStep;
+    return tree::segment_steps(steps, (nodes + NT - 1) / NT * Hkv) * tree::kStep;
+}
 
 size_t tree_ws_bytes(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t Dh, int32_t max_nodes, int32_t max_seq) {
     using namespace tree;

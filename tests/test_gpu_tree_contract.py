@@ -229,3 +229,22 @@ def test_a_wait_that_runs_out_is_reported_and_the_stream_recovers(bi, H, Hkv, Dh
                                 out_dtype=bi.F32, ws=ws, out=out, status=st, wait_limit_ns=100_000_000, skip_copy=-1)
     bi.check_status(st)
     assert same_bits(out, want)
+
+
+# ---- the cut of a request's keys --------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("H,Hkv,Dh", [(8, 1, 64), (16, 2, 128), (32, 8, 128), (16, 16, 64)])
+@pytest.mark.parametrize("steps", [1, 2, 16, 17, 64, 65, 130])
+def test_cuts_of_every_length_within_the_workspace(bi, H, Hkv, Dh, steps):
+    """Requests that end on, before and after a step, on both sides of the cut's thresholds, in exactly the workspace
+    that the call asks for; nothing behind it is written."""
+    ends = [128 * steps - 127, 128 * steps - 1, 128 * steps]
+    nodes = [min(n, e) for n, e in zip((1, 40, 9), ends)]
+    c = TreeCase([e - n for e, n in zip(ends, nodes)], nodes, H, Hkv, Dh, 80 + steps)
+    need = bi.tree_attention_workspace_size(3, sum(nodes), H, Hkv, Dh, c.max_nodes, c.max_seq)
+    buf = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    st = bi.new_status()
+    out = c.run(bi, out_dtype=bi.F32, ws=buf[:need], status=st)
+    bi.check_status(st)
+    close(out, c.ref(), torch.float32)
+    assert (buf[need:] == 77).all()
