@@ -421,8 +421,8 @@ bi_status bi_qk_norm_rope_append(const void* qkv, bi_dtype qkv_dtype, const bi_b
  * max_seq_len: HOST bound on pos0[r] + nodes (0 < max_seq_len <= max_pages *
  * 16); a request outside its bounds gets zeros (BI_DEV_BAD_POSITION).
  * ws: DEVICE scratch of bi_tree_attention_workspace_size bytes, 16-byte
- * aligned.  Supported: Dh in {64, 128}, H / Hkv in {1, 2, 4, 8}.  scale <= 0
- * (or NaN) selects the default, as in bi_decode_attention. */
+ * aligned.  Supported: Dh in {64, 128}, H / Hkv in {1, 2, 4, 8}, Hkv <= 65535.
+ * scale <= 0 (or NaN) selects the default, as in bi_decode_attention. */
 size_t bi_tree_attention_workspace_size(int32_t B, int32_t T, int32_t H, int32_t Hkv, int32_t Dh, int32_t max_nodes,
                                         int32_t max_seq_len);
 /* Positions of a segment of a request with so many positions (context and

@@ -13,6 +13,7 @@ namespace {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool aligned16(const void* p) { return aligned(p, 16); }
 constexpr int32_t kMaxPages = 0x7fffffff / BI_PAGE;  // a slot (16 * page + offset) is an int32
+constexpr int32_t kMaxTreeHeads = 65535;              // KV heads are a grid's y extent
 }  // namespace
 
 static bi_status run_build_slots(const char* name, bool pad, const int32_t* q_len, const int32_t* pos0,
@@ -104,6 +105,7 @@ static bi_status run_tree_attention(const bi_bf16* q, const int32_t* cu_q, const
     if (B < 0 || T < 0) return fail(BI_ERR_SHAPE, "bi_tree_attention: negative size");
     if (!attention_supported(H, Hkv, Dh))
         return fail(BI_ERR_UNSUPPORTED, "bi_tree_attention: need Dh in {64,128} and H/Hkv in {1,2,4,8}");
+    if (Hkv > kMaxTreeHeads) return fail(BI_ERR_SHAPE, "bi_tree_attention: need Hkv <= 65535");
     if (max_nodes <= 0 || max_nodes > BI_TREE_MAX_NODES || mask_words < (max_nodes + 31) / 32)
         return fail(BI_ERR_SHAPE, "bi_tree_attention: need 0 < max_nodes <= 256 and mask_words * 32 >= max_nodes");
     if (max_pages <= 0 || num_pages <= 0 || max_pages > kMaxPages || num_pages > kMaxPages)
