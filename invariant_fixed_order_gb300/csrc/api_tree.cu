@@ -21,20 +21,20 @@ static bi_status run_build_slots(const char* name, bool pad, const int32_t* q_le
                                  const int32_t* free_head, int32_t* free_head_out, const int32_t* depth, int32_t* cu_q,
                                  int32_t* tok_req, int32_t* tok_pos, int32_t* slots, int32_t B, int32_t T,
                                  int32_t max_pages, int32_t num_pages, int32_t* dev_status, bi_stream stream) {
-    const std::string n(name);
-    if (B < 0 || T < 0 || n_free < 0) return fail(BI_ERR_SHAPE, n + ": negative size");
+    const auto bad = [name](bi_status st, const char* what) { return fail(st, std::string(name) + what); };
+    if (B < 0 || T < 0 || n_free < 0) return bad(BI_ERR_SHAPE, ": negative size");
     if (max_pages <= 0 || num_pages <= 0 || max_pages > kMaxPages || num_pages > kMaxPages)
-        return fail(BI_ERR_SHAPE, n + ": need 0 < max_pages, num_pages < 2^27");
+        return bad(BI_ERR_SHAPE, ": need 0 < max_pages, num_pages < 2^27");
     if (!free_head || !free_head_out || !cu_q || (n_free > 0 && !free_pages) || (B > 0 && (!q_len || !pos0 || !page_table)) ||
         (T > 0 && (!tok_req || !tok_pos || !slots)))
-        return fail(BI_ERR_INVALID, n + ": null pointer");
+        return bad(BI_ERR_INVALID, ": null pointer");
     const void* all[] = {q_len, pos0, page_table, free_pages, free_head, free_head_out, depth, cu_q, tok_req, tok_pos, slots};
     for (const void* p : all)
-        if (!aligned(p, 4)) return fail(BI_ERR_INVALID, n + ": pointers must be 4-byte aligned");
+        if (!aligned(p, 4)) return bad(BI_ERR_INVALID, ": pointers must be 4-byte aligned");
     cudaError_t e = launch_build_slots(q_len, pos0, page_table, free_pages, n_free, free_head, free_head_out, depth, cu_q,
                                        tok_req, tok_pos, slots, pad, B, T, max_pages, num_pages, dev_status,
                                        static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? BI_OK : cuda_fail(e, (n + " launch").c_str());
+    return e == cudaSuccess ? BI_OK : cuda_fail(e, (std::string(name) + " launch").c_str());
 }
 
 extern "C" bi_status bi_build_slots(const int32_t* q_len, const int32_t* pos0, int32_t* page_table,
