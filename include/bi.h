@@ -337,7 +337,8 @@ bi_status bi_embed(const bi_bf16* E, const int32_t* ids, bi_bf16* x, int32_t T, 
  * behind its context in the order the drafter gives them, so siblings share a
  * rotation angle (the position their path gives them) but no cache slot.  The
  * four calls below take such a step from request lengths to scored nodes; they
- * serve plain decode and prefill steps as well (a chain is a tree).  Each is
+ * serve plain decode and prefill steps as well (a chain is a tree: the values of
+ * decode and prefill attention, with bits of their own).  Each is
  * batch invariant: a row's bits depend on its own request alone.
  *
  * bi_build_slots: page tables and slot maps from request lengths, on the GPU.
@@ -408,7 +409,8 @@ bi_status bi_qk_norm_rope_append(const void* qkv, bi_dtype qkv_dtype, const bi_b
  * q: DEVICE [T, H, Dh] bf16; out: DEVICE [T, H, Dh].  A node with nothing to
  * attend gets zeros; rows at or past cu_q[B] are left as they were.
  * Positions a node does not attend contribute nothing, whatever the cache
- * holds there (NaN and infinities included).
+ * holds there (NaN and infinities included); a value that is not finite makes
+ * its dimension not finite for every node that attends it.
  * Arithmetic: scores in fp32 (bf16 products), softmax statistics and sums in
  * fp32; the weights p = 2^(score - reference) multiply V as bf16 hi + lo parts;
  * a bf16 output is the fp32 output, rounded once.  A request's positions are
@@ -419,7 +421,8 @@ bi_status bi_qk_norm_rope_append(const void* qkv, bi_dtype qkv_dtype, const bi_b
  * its draft, and are not those of bi_decode_attention or bi_prefill_attention
  * over the same keys (a chain gets their values, not their bits).
  * max_seq_len: HOST bound on pos0[r] + nodes (0 < max_seq_len <= max_pages *
- * 16); a request outside its bounds gets zeros (BI_DEV_BAD_POSITION).
+ * 16); a request outside its bounds gets zeros (BI_DEV_BAD_POSITION); one whose
+ * cu_q entries do not ascend within 0..T is reported alike and has no rows.
  * ws: DEVICE scratch of bi_tree_attention_workspace_size bytes, 16-byte
  * aligned.  Supported: Dh in {64, 128}, H / Hkv in {1, 2, 4, 8}, Hkv <= 65535.
  * scale <= 0 (or NaN) selects the default, as in bi_decode_attention. */

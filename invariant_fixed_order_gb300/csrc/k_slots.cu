@@ -19,7 +19,7 @@ namespace bi {
 // is between reading free_head everywhere and writing free_head_out: where they
 // are one word the CTAs are a cluster and meet at its barrier.  Requests are
 // taken kSlotThreads at a time, so B has no limit.  Measured: 64 requests, one
-// token each 3.7 us (the launch); 512 requests, 131 k tokens 8.0 us as a
+// token each 3.9 us (the launch); 512 requests, 131 k tokens 8.1 us as a
 // grid, 22 us as a cluster.
 // ---------------------------------------------------------------------------
 constexpr int kSlotThreads = 1024;
@@ -204,8 +204,9 @@ cudaError_t launch_build_slots(const int32_t* q_len, const int32_t* pos0, int32_
 // one token; its lanes keep the token's cos and sin for all their heads.  With
 // fewer tokens than SMs a token's heads go to several CTAs, each with one sweep
 // of them.  Bound by HBM: each element is read once and written once.  Measured
-// on 411 MB (fp32, 32 + 16 heads of 128, norms): 70.8 us with 64 threads, 5.8
-// TB/s; 74.1 with 128, 100 with 256, whose last sweep leaves lanes idle.
+// on 411 MB (16384 tokens, bf16, 32 + 16 heads of 128, norms): 71.6 us with 64
+// threads, 5.7 TB/s; 74.1 with 128, 100 with 256, whose last sweep leaves lanes
+// idle.
 // ---------------------------------------------------------------------------
 constexpr int kQkThreads = 64;
 

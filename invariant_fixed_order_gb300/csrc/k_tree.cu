@@ -36,18 +36,19 @@
 // columns without a wait of their own.
 //
 // Bound.  Lone tiles by HBM: a step's 64 KB of K and V take one SM's share of
-// the copy bandwidth 1.45 us.  Pairs of tiles by that and by the softmax warps
-// alike: a half step takes a lane's warps 1650 cycles (420 to load 64 scores and
-// find the maximum, 700 for 64 exponentials, the rest waits and stores), 3300 a
-// step of two tiles against 2900 for its bytes.  Measured (32 query heads, 8 KV
-// heads, Dh 128): 16 requests with up to 16 nodes over up to 8192 positions
-// 73 us (46 for the bytes), 64 requests with 33 to 64 nodes 326 us (186).  What
-// remains is the ranges' unequal ends (runs are whole segments; 10 to 20 %),
-// the partials, and a CTA's start and end.
+// the copy bandwidth 1.5 us.  Pairs of tiles by the softmax warps: they take a
+// half step's scores, exponentials and parts of P one after the other, while the
+// tensor pipe is busy for 47 % of the cycles and DRAM for 42 (24 requests).
+// Measured (32 query heads, 8 KV heads, Dh 128): 16 requests with up to 16 nodes
+// over up to 8192 positions 79 us (46 for the bytes), 64 requests with 33 to 64
+// nodes 390 us (188).  What remains is the ranges' unequal ends (runs are whole
+// segments; 10 to 20 %), the partials, and a CTA's start and end.  P's lo part is
+// 6 and 66 us of it.
 //
-// What the other layouts measured on the 16 / 64 requests: one lane whose two
-// warpgroups take steps in turn 78 / 508 us (each tile copies its keys again);
-// O in registers, 16 warps with four threads to a row 96 / 538.
+// What the other layouts measured on the 16 / 64 requests, with P in one part
+// (73 / 326 us in this one): one lane whose two warpgroups take steps in turn 78 /
+// 508 us (each tile copies its keys again); O in registers, 16 warps with four
+// threads to a row 96 / 538.
 #include <math.h>
 
 #include <mutex>
